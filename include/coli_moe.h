@@ -220,6 +220,79 @@ int coli_moe_layer_profiled(const coli_moe_cfg *cfg, const coli_moe_weights *w, 
 int coli_moe_num_stages(void);
 const char *coli_moe_stage_name(int32_t stage);
 
+/* ---- The route from logits, and products whose both operands are MXFP4 ----
+ * Both follow the conventions at the top of this header. Element types of x, logits, h and
+ * outputs: coli_dtype. Activations are quantised to MXFP4 inside the products:
+ *   MXFP4 of a block of 32 values b (JustVugg/colibri README, "Other supported models", names
+ *   the format; OCP MX v1.0): E8M0 byte u = max(floor(log2 max|b|) - 2 + 127, 0), 0 for a
+ *   block of zeros; codes E2M1 of b / 2^(u - 127), to nearest, ties to even, saturating at 6.
+ *   A block that holds an infinity or a NaN has u = 255 (NaN) and codes 0.
+ * Sums are fp32, in an order fixed by the shapes (no atomics); outputs are rounded once. */
+typedef enum { COLI_F32 = 0, COLI_BF16 = 1, COLI_F16 = 2 } coli_dtype;
+typedef enum { COLI_SCORE_SIGMOID = 0, COLI_SCORE_SOFTMAX = 1 } coli_score;
+
+/* A router over given logits. Limits: 1 <= n_experts <= 1024; n_experts % n_group == 0;
+ * 1 <= topk_group <= n_group <= 64; 1 <= top_k <= min(64, topk_group * n_experts / n_group). */
+typedef struct {
+  int32_t n_experts;  /* E */
+  int32_t top_k;      /* k */
+  int32_t n_group;    /* G contiguous groups of E/G experts */
+  int32_t topk_group; /* Gk groups kept */
+  int32_t group_top;  /* a group counts by its best (1) or by the sum of its two best (2) */
+  int32_t score;      /* coli_score */
+  int32_t renorm;     /* 1: weights over their sum */
+  float scale;        /* multiplies every weight */
+} coli_moe_router;
+
+/* The route of T tokens from logits z [T][E] (aligned to their type): an expert is present
+ * for a token unless its logit is -inf or NaN; p = sigmoid(z), or softmax(z) over the experts
+ * present (those of logit +inf share everything), in fp64; key = z, or p + bias[e] with a bias
+ * (fp32 [E], NULL: none; a bias of -inf or NaN takes its expert away). With n_group > 1 a
+ * group counts by its best key (group_top 1, or groups of one) or by the sum of its two best
+ * p (+ bias), absent experts left out; the topk_group best groups are kept. topk_idx int32
+ * [T][k] = the k best keys of the kept groups in descending order, every tie to the lower
+ * index; topk_w fp32 [T][k] = p, with renorm over the sum of the taken (0 where that is 0),
+ * times scale. Slots that no expert is left for hold -1 and 0, which coli_moe_group takes.
+ * Follows colibri-strix README, "What's implemented", router item. */
+int coli_moe_route_logits(const coli_moe_router *r, const void *z, int dtype, int32_t T, const float *bias,
+                          int32_t *topk_idx, float *topk_w, void *stream);
+
+/* MXFP4 of rows x cols values (cols % 32 == 0; x and codes 16-byte aligned): codes
+ * [rows][cols/2], scales [rows][cols/32]; and back, value = e2m1(code) * 2^(u - 127) rounded
+ * to dtype (NaN for u = 255; out 16-byte aligned). */
+int coli_moe_mxfp4_quantize(const void *x, int dtype, int64_t rows, int32_t cols, uint8_t *codes, uint8_t *scales,
+                            void *stream);
+int coli_moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols, void *out,
+                              int dtype, void *stream);
+
+/* y [M][N] = MXFP4(x [M][K]) W^T, W's N rows given as codes [N][K/2] (16-byte aligned) and
+ * scales [N][K/32] (any alignment). K % 32 == 0, x and y 16-byte aligned, y of x's dtype.
+ * workspace: coli_moe_mxfp4_linear_workspace_bytes(M_max, N, K), 256-byte aligned, for every
+ * M <= M_max (0 if a size is invalid; M = 0 or N = 0: a no-op). */
+size_t coli_moe_mxfp4_linear_workspace_bytes(int32_t M_max, int32_t N, int32_t K);
+int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const uint8_t *scales, int32_t M, int32_t N,
+                          int32_t K, void *y, void *workspace, size_t ws_bytes, void *stream);
+
+/* The two halves of the expert FFN over a route and its grouping (coli_moe_group's arrays for
+ * the same T), every product MXFP4 x MXFP4. cfg->wfmt = COLI_W_MXFP4; its router fields, topp
+ * and routed_scaling_factor are not read beyond their validation.
+ *   gate_up: h [T k + T has_shared][F], row t k + j = silu(g) * u of the expert of slot j of
+ *     token t, row T k + t the shared expert's. Rows of empty slots (-1) are not written.
+ *   down: out [T][H] = sum_j w_tj y_tj in slot order + y_shared, y = down rows . MXFP4(h row);
+ *     h rows of empty slots do not enter.
+ * x, h, out of one dtype and 16-byte aligned. workspace:
+ * coli_moe_mxfp4_experts_workspace_bytes(cfg, T_max) (0 if invalid), 256-byte aligned, for
+ * either half and every T <= T_max.
+ * Follow the batch-union item of colibri-strix README, "What's implemented". */
+size_t coli_moe_mxfp4_experts_workspace_bytes(const coli_moe_cfg *cfg, int32_t T_max);
+int coli_moe_mxfp4_gate_up(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *x, int dtype, int32_t T,
+                           const int32_t *expert_off, const int32_t *pair_perm, const int32_t *active,
+                           const int32_t *n_active, void *h, void *workspace, size_t ws_bytes, void *stream);
+int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *h, int dtype, int32_t T,
+                        const int32_t *topk_idx, const float *topk_w, const int32_t *expert_off,
+                        const int32_t *pair_perm, const int32_t *active, const int32_t *n_active, void *out,
+                        void *workspace, size_t ws_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *coli_moe_strerror(int status);
 

@@ -7,6 +7,8 @@ library is not built, importing any entry point raises.
 Entry points (same names as the C ABI in include/coli_moe.h):
     quantize_q8_0, route, group, ffn, layer, layer_noalloc, layer_profiled,
     blob_bytes, workspace_bytes, scratch_bytes, num_stages, stage_name, strerror;
+    route_logits, mxfp4_quantize, mxfp4_dequantize, mxfp4_linear, mxfp4_gate_up,
+    mxfp4_down (with make_router and the alloc_mxfp4_*_workspace helpers);
 plus TimingEvents (HIP events for layer_profiled) and alloc_workspace.
 Tensors must be CUDA tensors, contiguous, with the dtypes documented in the header.
 """
@@ -97,6 +99,22 @@ EXPORTS = {
     "coli_moe_layer_profiled": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p,
                                           C.c_void_p, C.c_size_t, C.c_void_p, C.POINTER(C.c_void_p),
                                           C.c_int32]),
+    "coli_moe_route_logits": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_void_p]),
+    "coli_moe_mxfp4_quantize": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int32, C.c_void_p, C.c_void_p,
+                                          C.c_void_p]),
+    "coli_moe_mxfp4_dequantize": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int,
+                                            C.c_void_p]),
+    "coli_moe_mxfp4_linear_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32]),
+    "coli_moe_mxfp4_linear": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
+                                        C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "coli_moe_mxfp4_experts_workspace_bytes": (C.c_size_t, [C.c_void_p, C.c_int32]),
+    "coli_moe_mxfp4_gate_up": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p,
+                                         C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                         C.c_void_p]),
+    "coli_moe_mxfp4_down": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                      C.c_size_t, C.c_void_p]),
     "coli_moe_num_stages": (C.c_int, []),
     "coli_moe_stage_name": (C.c_char_p, [C.c_int32]),
     "coli_moe_strerror": (C.c_char_p, [C.c_int]),
@@ -410,3 +428,144 @@ def tier_prefetch(cfg: Cfg, w: Weights, tier: Tier, host_experts, host_scales, p
                                         _ptr(x), x.shape[0], _ptr(workspace), workspace.numel(), _stream(stream, x),
                                         C.c_void_p(copy_stream.cuda_stream), C.byref(n)), "coli_moe_tier_prefetch")
     return n.value
+
+
+# ------------------------------------------------------------------ route from logits, MXFP4 x MXFP4
+class Router(C.Structure):
+    """coli_moe_router."""
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("n_group", C.c_int32), ("topk_group", C.c_int32),
+                ("group_top", C.c_int32), ("score", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
+
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def make_router(n_experts, top_k, n_group=1, topk_group=1, score="sigmoid", group_top=2, renorm=True,
+                scale=1.0) -> Router:
+    """A router over given logits: score "sigmoid" or "softmax"; a group counts by its best
+    expert (group_top 1) or the sum of its two best (2); weights over their sum with renorm."""
+    if score not in _SCORES:
+        raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
+    return Router(n_experts, top_k, n_group, topk_group, group_top, _SCORES[score], int(bool(renorm)), scale)
+
+
+def _elem(t, name) -> int:
+    """coli_dtype of a tensor."""
+    import torch
+    d = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
+    return d
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def route_logits(router: Router, logits, topk_idx, topk_w, bias=None, stream=None):
+    """coli_moe_route_logits: logits [T][E] (fp32, bf16 or fp16) -> topk_idx int32, topk_w fp32 [T][k]."""
+    import torch
+    d = _elem(logits, "logits")
+    _dt(topk_idx, torch.int32, "topk_idx"), _dt(topk_w, torch.float32, "topk_w")
+    T = logits.shape[0]
+    _shape(logits, (T, router.n_experts), "logits")
+    _shape(topk_idx, (T, router.top_k), "topk_idx"), _shape(topk_w, (T, router.top_k), "topk_w")
+    if bias is not None:
+        _dt(bias, torch.float32, "bias"), _shape(bias, (router.n_experts,), "bias")
+    _check(lib().coli_moe_route_logits(C.byref(router), _ptr(logits), d, T, _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
+                                       _stream(stream, logits)), "coli_moe_route_logits")
+
+
+def _mx_shapes(rows, cols, codes, scales):
+    import torch
+    _dt(codes, torch.uint8, "codes"), _dt(scales, torch.uint8, "scales")
+    _shape(codes, (rows, cols // 2), "codes"), _shape(scales, (rows, cols // 32), "scales")
+
+
+def mxfp4_quantize(x, codes, scales, stream=None):
+    """coli_moe_mxfp4_quantize: x [rows][cols] -> codes uint8 [rows][cols/2], scales uint8 [rows][cols/32]."""
+    rows, cols = x.shape
+    d = _elem(x, "x")
+    _mx_shapes(rows, cols, codes, scales)
+    _check(lib().coli_moe_mxfp4_quantize(_ptr(x), d, rows, cols, _ptr(codes), _ptr(scales), _stream(stream, x)),
+           "coli_moe_mxfp4_quantize")
+
+
+def mxfp4_dequantize(codes, scales, out, stream=None):
+    """coli_moe_mxfp4_dequantize: codes, scales -> the values they stand for, out [rows][cols]."""
+    rows, cols = out.shape
+    d = _elem(out, "out")
+    _mx_shapes(rows, cols, codes, scales)
+    _check(lib().coli_moe_mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), d, _stream(stream, out)),
+           "coli_moe_mxfp4_dequantize")
+
+
+def alloc_mxfp4_linear_workspace(M_max: int, N: int, K: int, device="cuda"):
+    import torch
+    n = int(lib().coli_moe_mxfp4_linear_workspace_bytes(M_max, N, K))
+    if n == 0:
+        raise ColiError(COLI_E_UNSUPPORTED, "coli_moe_mxfp4_linear_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mxfp4_linear(x, codes, scales, out, workspace, stream=None):
+    """coli_moe_mxfp4_linear: out [M][N] = MXFP4(x [M][K]) W^T, W = codes [N][K/2] with scales [N][K/32]."""
+    M, K = x.shape
+    N = codes.shape[0]
+    d = _elem(x, "x")
+    _dt(out, x.dtype, "out"), _shape(out, (M, N), "out")
+    _mx_shapes(N, K, codes, scales)
+    _check(lib().coli_moe_mxfp4_linear(_ptr(x), d, _ptr(codes), _ptr(scales), M, N, K, _ptr(out), _ptr(workspace),
+                                       workspace.numel(), _stream(stream, x)), "coli_moe_mxfp4_linear")
+
+
+def alloc_mxfp4_experts_workspace(cfg: Cfg, T_max: int, device="cuda"):
+    import torch
+    n = int(lib().coli_moe_mxfp4_experts_workspace_bytes(C.byref(cfg), T_max))
+    if n == 0:
+        raise ColiError(COLI_E_UNSUPPORTED, "coli_moe_mxfp4_experts_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _mx_experts(cfg, w, T, off, perm, active, n_active):
+    import torch
+    E, S = cfg.n_experts, cfg.has_shared
+    n = 3 * cfg.hidden * cfg.ffn
+    _dt(w.experts, torch.uint8, "experts"), _dt(w.scales, torch.uint8, "scales")
+    if w.experts.numel() != (E + S) * (n // 2) or w.scales.numel() != (E + S) * (n // 32):
+        raise ValueError("weights: sizes do not match the configuration")
+    for name, t, size in (("off", off, E + 1), ("perm", perm, T * cfg.top_k), ("active", active, E),
+                          ("n_active", n_active, 1)):
+        _dt(t, torch.int32, name)
+        if t.numel() != size:
+            raise ValueError(f"{name}: expected {size} elements, got {t.numel()}")
+
+
+def mxfp4_gate_up(cfg: Cfg, w: Weights, x, off, perm, active, n_active, h, workspace, stream=None):
+    """coli_moe_mxfp4_gate_up: h [T k + T shared][F] = silu(gate) * up of every pair of the route."""
+    T = x.shape[0]
+    d = _elem(x, "x")
+    _shape(x, (T, cfg.hidden), "x"), _dt(h, x.dtype, "h")
+    _shape(h, (T * (cfg.top_k + cfg.has_shared), cfg.ffn), "h")
+    _mx_experts(cfg, w, T, off, perm, active, n_active)
+    wc = w.c()
+    _check(lib().coli_moe_mxfp4_gate_up(C.byref(cfg), C.byref(wc), _ptr(x), d, T, _ptr(off), _ptr(perm), _ptr(active),
+                                        _ptr(n_active), _ptr(h), _ptr(workspace), workspace.numel(),
+                                        _stream(stream, x)), "coli_moe_mxfp4_gate_up")
+
+
+def mxfp4_down(cfg: Cfg, w: Weights, h, topk_idx, topk_w, off, perm, active, n_active, out, workspace, stream=None):
+    """coli_moe_mxfp4_down: out [T][H] = the pairs' down rows, weighted and summed, + the shared expert's."""
+    import torch
+    T = topk_idx.shape[0]
+    d = _elem(h, "h")
+    _shape(h, (T * (cfg.top_k + cfg.has_shared), cfg.ffn), "h"), _dt(out, h.dtype, "out")
+    _shape(out, (T, cfg.hidden), "out")
+    _dt(topk_idx, torch.int32, "topk_idx"), _dt(topk_w, torch.float32, "topk_w")
+    _shape(topk_idx, (T, cfg.top_k), "topk_idx"), _shape(topk_w, (T, cfg.top_k), "topk_w")
+    _mx_experts(cfg, w, T, off, perm, active, n_active)
+    wc = w.c()
+    _check(lib().coli_moe_mxfp4_down(C.byref(cfg), C.byref(wc), _ptr(h), d, T, _ptr(topk_idx), _ptr(topk_w), _ptr(off),
+                                     _ptr(perm), _ptr(active), _ptr(n_active), _ptr(out), _ptr(workspace),
+                                     workspace.numel(), _stream(stream, h)), "coli_moe_mxfp4_down")

@@ -85,6 +85,11 @@ struct WsLayout {
 // Workspace layout for T tokens (valid cfg assumed).
 WsLayout ws_layout(const coli_moe_cfg &c, int32_t T, int32_t ksplit);
 
+// Host-side validation shared by the entry points: a coli_status.
+int check_cfg(const coli_moe_cfg *c);
+int check_T(const coli_moe_cfg *c, int32_t T);
+int check_weights(const coli_moe_weights *w, bool need_experts, bool need_router);
+
 // number of K splits of the router logits for T tokens
 int32_t route_ksplit(const coli_moe_cfg &c, int32_t T);
 
@@ -208,6 +213,42 @@ int route_phase(const coli_moe_cfg *cfg, const coli_moe_weights *w, const float 
 // Where a workspace for T tokens holds the Q8_0 of x (the same for every cfg of hidden H).
 int8_t *ws_xq(const coli_moe_cfg &c, int32_t T, void *ws);
 float *ws_xd(const coli_moe_cfg &c, int32_t T, void *ws);
+
+// ---- MXFP4 x MXFP4 operators (mxfp4_*.hip) and the route from logits (route_logits.hip)
+struct RouteLogitsArgs {
+  int32_t T, E, k, G, Gk, group_top, softmax, renorm;
+  float scale;
+  const float *bias;  // null: none
+  int32_t *idx;       // [T][k] out
+  float *w;           // [T][k] out
+};
+hipError_t launch_route_logits(const RouteLogitsArgs &a, const void *z, int dtype, hipStream_t s);
+
+// Quantised activations are held with their rows padded to a multiple of the K stage.
+constexpr int MX_KSTAGE = 256;
+__host__ __device__ inline int mx_padded(int K) { return (K + MX_KSTAGE - 1) / MX_KSTAGE * MX_KSTAGE; }
+
+enum MxMode { MX_LINEAR, MX_GATEUP, MX_DOWN };
+
+struct MxArgs {
+  const uint8_t *wc, *ws;         // weight codes and E8M0 bytes (expert 0)
+  int64_t wc_stride, ws_stride;   // bytes per expert
+  int32_t N, K;                   // output columns (weight rows of a matrix), inputs
+  const uint8_t *ac, *as;         // quantised activations, rows of mx_padded(K)
+  int32_t M;                      // rows (linear); tokens (experts)
+  int32_t E, k, has_shared;       // experts only, as is the grouping below
+  const int32_t *off, *perm, *active, *nact;
+  void *out;                      // linear [M][N], gate/up h [pairs][N], down fp32 [pairs][N]
+};
+
+hipError_t launch_mx_quantize(const void *x, int dtype, int64_t nblk, uint8_t *codes, uint8_t *scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t nblk, void *out, int dtype,
+                                hipStream_t s);
+hipError_t launch_mx_quantize_rows(const void *x, int dtype, int64_t rows, int K, uint8_t *codes, uint8_t *scales,
+                                   hipStream_t s);
+hipError_t launch_mx_product(MxMode mode, int dtype, const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_combine(const float *y, const int32_t *idx, const float *w, int T, int k, int E, int H,
+                             int has_shared, void *out, int dtype, hipStream_t s);
 
 hipError_t launch_combine(const float *ypair, const float *w, int32_t T, int32_t k, int32_t H,
                           int32_t has_shared, float *out, hipStream_t s);

@@ -46,7 +46,7 @@ static size_t gemv_lds(int K) {
          2 * GEMV_NT * sizeof(int);
 }
 
-static int check_cfg(const coli_moe_cfg *c) {
+int check_cfg(const coli_moe_cfg *c) {
   if (!c) return COLI_E_INVALID;
   if (c->hidden <= 0 || c->ffn <= 0 || c->n_experts <= 0 || c->top_k <= 0 || c->n_group <= 0 ||
       c->topk_group <= 0)
@@ -67,7 +67,7 @@ static int check_cfg(const coli_moe_cfg *c) {
   return COLI_OK;
 }
 
-static int check_T(const coli_moe_cfg *c, int32_t T) {
+int check_T(const coli_moe_cfg *c, int32_t T) {
   if (T < 0) return COLI_E_INVALID;
   if ((int64_t)T * c->top_k > 65535) return COLI_E_UNSUPPORTED;
   if (T > 0 && !group_supported(T * c->top_k, c->n_experts)) return COLI_E_UNSUPPORTED;
@@ -76,7 +76,7 @@ static int check_T(const coli_moe_cfg *c, int32_t T) {
 
 static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-static int check_weights(const coli_moe_weights *w, bool need_experts, bool need_router) {
+int check_weights(const coli_moe_weights *w, bool need_experts, bool need_router) {
   if (!w) return COLI_E_INVALID;
   if (need_experts) {
     if (!w->experts || !w->scales) return COLI_E_INVALID;

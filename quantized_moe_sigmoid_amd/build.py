@@ -21,7 +21,7 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
 HIP_FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++20", "-fPIC",
     # packed fp32 instructions stay off (v_pk_*_f32 are not generated)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # fp32 division correctly rounded: Q8_0 codes are defined by x / d

@@ -228,16 +228,21 @@ hipError_t launch_route_logits(const RouteLogitsArgs &a, const void *z, int dtyp
 constexpr int MX_KSTAGE = 256;
 __host__ __device__ inline int mx_padded(int K) { return (K + MX_KSTAGE - 1) / MX_KSTAGE * MX_KSTAGE; }
 
+constexpr int MX_ROWS_TILE = 127;  // a dense product of more rows takes the tiled kernel
+
 enum MxMode { MX_LINEAR, MX_GATEUP, MX_DOWN };
 
 struct MxArgs {
   const uint8_t *wc, *ws;         // weight codes and E8M0 bytes (expert 0)
   int64_t wc_stride, ws_stride;   // bytes per expert
+  int32_t ws_pitch;               // bytes of scales per weight row
   int32_t N, K;                   // output columns (weight rows of a matrix), inputs
   const uint8_t *ac, *as;         // quantised activations, rows of mx_padded(K)
   int32_t M;                      // rows (linear); tokens (experts)
   int32_t E, k, has_shared;       // experts only, as is the grouping below
   const int32_t *off, *perm, *active, *nact;
+  int4 *tiles;                    // row tiles of the route (tiled experts only) and their number
+  int32_t *ntiles;
   void *out;                      // linear [M][N], gate/up h [pairs][N], down fp32 [pairs][N]
 };
 
@@ -246,7 +251,11 @@ hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int
                                 hipStream_t s);
 hipError_t launch_mx_quantize_rows(const void *x, int dtype, int64_t rows, int K, uint8_t *codes, uint8_t *scales,
                                    hipStream_t s);
+// rows of nb scale bytes copied to a pitch of mx_padded(32 nb) / 32, the rest set to 1
+hipError_t launch_mx_pad_scales(const uint8_t *scales, int rows, int K, uint8_t *out, hipStream_t s);
 hipError_t launch_mx_product(MxMode mode, int dtype, const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_tile(MxMode mode, int dtype, const MxArgs &a, hipStream_t s);
+int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared);  // most row tiles of a route
 hipError_t launch_mx_combine(const float *y, const int32_t *idx, const float *w, int T, int k, int E, int H,
                              int has_shared, void *out, int dtype, hipStream_t s);
 

@@ -10,27 +10,36 @@ static int mx_dev(hipError_t e) { return e == hipSuccess ? COLI_OK : COLI_E_DEVI
 static bool mx_dtype(int d) { return d == COLI_F32 || d == COLI_BF16 || d == COLI_F16; }
 static size_t mx_al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// A workspace: quantised activations (codes, E8M0 bytes), then the down product's fp32 rows.
+// A workspace: quantised activations (codes, E8M0 bytes), the row tiles of a route, then the
+// down product's fp32 rows or a dense product's padded weight scales.
 struct MxWs {
-  size_t ac, as, y, total;
+  size_t ac, as, tiles, ntiles, y, total;
 };
 
-static MxWs mx_ws(int64_t rows, int K, size_t y_bytes) {
+static MxWs mx_ws(int64_t rows, int K, int64_t tiles, size_t y_bytes) {
   MxWs L{};
   const size_t kp = (size_t)mx_padded(K);
   size_t o = 0;
   L.ac = o;  o = mx_al256(o + rows * (kp / 2));
   L.as = o;  o = mx_al256(o + rows * (kp / 32));
+  L.tiles = o;   o = mx_al256(o + tiles * sizeof(int4));
+  L.ntiles = o;  o = mx_al256(o + (tiles ? sizeof(int32_t) : 0));
   L.y = o;   o = mx_al256(o + y_bytes);
   L.total = o;
   return L;
 }
 
 static int64_t mx_rows(const coli_moe_cfg &c, int32_t T) { return (int64_t)T * (c.top_k + c.has_shared); }
-static MxWs mx_ws_gateup(const coli_moe_cfg &c, int32_t T) { return mx_ws(T, c.hidden, 0); }
+static int64_t mx_tiles(const coli_moe_cfg &c, int32_t T) {
+  return mx_tile_cap(T, c.top_k, c.n_experts, c.has_shared);
+}
+static MxWs mx_ws_gateup(const coli_moe_cfg &c, int32_t T) { return mx_ws(T, c.hidden, mx_tiles(c, T), 0); }
 static MxWs mx_ws_down(const coli_moe_cfg &c, int32_t T) {
   const int64_t R = mx_rows(c, T);
-  return mx_ws(R, c.ffn, (size_t)R * c.hidden * sizeof(float));
+  return mx_ws(R, c.ffn, mx_tiles(c, T), (size_t)R * c.hidden * sizeof(float));
+}
+static MxWs mx_ws_linear(int32_t M, int32_t N, int32_t K) {
+  return mx_ws(M, K, 0, M > MX_ROWS_TILE ? (size_t)N * (mx_padded(K) / 32) : 0);
 }
 
 static int check_linear(int32_t M, int32_t N, int32_t K) {
@@ -63,6 +72,14 @@ static MxArgs expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
   a.active = active;
   a.nact = nact;
   return a;
+}
+
+static hipError_t launch_experts(MxMode mode, int dtype, MxArgs &a, uint8_t *ws, const MxWs &L, hipStream_t s) {
+  a.ws_pitch = a.K / 32;
+  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P) return launch_mx_product(mode, dtype, a, s);
+  a.tiles = reinterpret_cast<int4 *>(ws + L.tiles);
+  a.ntiles = reinterpret_cast<int32_t *>(ws + L.ntiles);
+  return launch_mx_tile(mode, dtype, a, s);
 }
 
 }  // namespace coli
@@ -127,7 +144,7 @@ int coli_moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64
 
 size_t coli_moe_mxfp4_linear_workspace_bytes(int32_t M_max, int32_t N, int32_t K) {
   if (check_linear(M_max, N, K) != COLI_OK) return 0;
-  return mx_ws(M_max > 0 ? M_max : 1, K, 0).total;
+  return mx_ws_linear(M_max > 0 ? M_max : 1, N, K).total;
 }
 
 int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const uint8_t *scales, int32_t M, int32_t N,
@@ -138,7 +155,7 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
   if (M == 0 || N == 0) return COLI_OK;
   if (!x || !codes || !scales || !y) return COLI_E_INVALID;
   if (!mx_aligned(x, 16) || !mx_aligned(codes, 16) || !mx_aligned(y, 16)) return COLI_E_ALIGN;
-  const MxWs L = mx_ws(M, K, 0);
+  const MxWs L = mx_ws_linear(M, N, K);
   if (!workspace || ws_bytes < L.total) return COLI_E_WORKSPACE;
   if (!mx_aligned(workspace, 256)) return COLI_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -153,7 +170,14 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
   a.as = ws + L.as;
   a.M = M;
   a.out = y;
-  return mx_dev(launch_mx_product(MX_LINEAR, dtype, a, s));
+  a.ws_pitch = K / 32;
+  if (M <= MX_ROWS_TILE) return mx_dev(launch_mx_product(MX_LINEAR, dtype, a, s));
+  if (K % 128 || !mx_aligned(scales, 4)) {  // the tiled kernel loads scales by the aligned dword
+    if ((st = mx_dev(launch_mx_pad_scales(scales, N, K, ws + L.y, s)))) return st;
+    a.ws = ws + L.y;
+    a.ws_pitch = mx_padded(K) / 32;
+  }
+  return mx_dev(launch_mx_tile(MX_LINEAR, dtype, a, s));
 }
 
 size_t coli_moe_mxfp4_experts_workspace_bytes(const coli_moe_cfg *cfg, int32_t T_max) {
@@ -185,7 +209,7 @@ int coli_moe_mxfp4_gate_up(const coli_moe_cfg *cfg, const coli_moe_weights *w, c
   a.ac = ws + L.ac;
   a.as = ws + L.as;
   a.out = h;
-  return mx_dev(launch_mx_product(MX_GATEUP, dtype, a, s));
+  return mx_dev(launch_experts(MX_GATEUP, dtype, a, ws, L, s));
 }
 
 int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *h, int dtype, int32_t T,
@@ -213,7 +237,7 @@ int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, cons
   a.ac = ws + L.ac;
   a.as = ws + L.as;
   a.out = ws + L.y;
-  if ((st = mx_dev(launch_mx_product(MX_DOWN, dtype, a, s)))) return st;
+  if ((st = mx_dev(launch_experts(MX_DOWN, dtype, a, ws, L, s)))) return st;
   return mx_dev(launch_mx_combine(reinterpret_cast<float *>(ws + L.y), topk_idx, topk_w, T, cfg->top_k,
                                   cfg->n_experts, cfg->hidden, cfg->has_shared, out, dtype, s));
 }

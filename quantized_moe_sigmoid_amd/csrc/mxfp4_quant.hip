@@ -77,6 +77,18 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(const T *__restri
   if (q == 0) scales[blk] = (uint8_t)u;
 }
 
+__global__ __launch_bounds__(256) void mx_pad_scales_kernel(const uint8_t *__restrict__ scales, int rows, int nb,
+                                                            int nbp, uint8_t *__restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // four bytes each
+  const int64_t row = i / (nbp / 4);
+  const int b0 = (int)(i - row * (nbp / 4)) * 4;
+  if (row >= rows) return;
+  uint32_t v = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) v |= (b0 + j < nb ? (uint32_t)scales[row * nb + b0 + j] : 127u) << (8 * j);
+  reinterpret_cast<uint32_t *>(out)[i] = v;
+}
+
 static unsigned grid_of(int64_t nblk) { return (unsigned)((nblk * 2 + 255) / 256); }
 
 hipError_t launch_mx_quantize(const void *x, int dtype, int64_t nblk, uint8_t *codes, uint8_t *scales, hipStream_t s) {
@@ -112,6 +124,13 @@ hipError_t launch_mx_quantize_rows(const void *x, int dtype, int64_t rows, int K
     hipLaunchKernelGGL(mx_quantize_rows_kernel<bf16_t>, g, b, 0, s, (const bf16_t *)x, rows, nb, nbp, codes, scales);
   else
     hipLaunchKernelGGL(mx_quantize_rows_kernel<f16_t>, g, b, 0, s, (const f16_t *)x, rows, nb, nbp, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_pad_scales(const uint8_t *scales, int rows, int K, uint8_t *out, hipStream_t s) {
+  const int nb = K / 32, nbp = mx_padded(K) / 32;
+  const int64_t n = (int64_t)rows * (nbp / 4);
+  hipLaunchKernelGGL(mx_pad_scales_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, scales, rows, nb, nbp, out);
   return hipGetLastError();
 }
 

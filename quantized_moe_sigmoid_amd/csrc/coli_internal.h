@@ -225,7 +225,7 @@ struct RouteLogitsArgs {
 hipError_t launch_route_logits(const RouteLogitsArgs &a, const void *z, int dtype, hipStream_t s);
 
 // Quantised activations are held with their rows padded to a multiple of the K stage.
-constexpr int MX_KSTAGE = 256;
+constexpr int MX_KSTAGE = 512;
 __host__ __device__ inline int mx_padded(int K) { return (K + MX_KSTAGE - 1) / MX_KSTAGE * MX_KSTAGE; }
 
 constexpr int MX_ROWS_TILE = 127;  // a dense product of more rows takes the tiled kernel

@@ -172,7 +172,7 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
   a.out = y;
   a.ws_pitch = K / 32;
   if (M <= MX_ROWS_TILE) return mx_dev(launch_mx_product(MX_LINEAR, dtype, a, s));
-  if (K % 128 || !mx_aligned(scales, 4)) {  // the tiled kernel loads scales by the aligned dword
+  if (K % 128 || K < 512 || !mx_aligned(scales, 4)) {  // the tiled kernel loads 16 scales at a dword's address
     if ((st = mx_dev(launch_mx_pad_scales(scales, N, K, ws + L.y, s)))) return st;
     a.ws = ws + L.y;
     a.ws_pitch = mx_padded(K) / 32;

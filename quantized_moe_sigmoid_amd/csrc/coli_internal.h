@@ -243,6 +243,7 @@ struct MxArgs {
   const int32_t *off, *perm, *active, *nact;
   int4 *tiles;                    // row tiles of the route (tiled experts only) and their number
   int32_t *ntiles;
+  int32_t strip;                  // column tiles that a workgroup runs one after another
   void *out;                      // linear [M][N], gate/up h [pairs][N], down fp32 [pairs][N]
 };
 

@@ -5,28 +5,28 @@
 
 namespace coli {
 
-// 16 (4) bytes from each lane's global address to consecutive LDS bytes at the wave-uniform
-// address lds, for the lanes of the mask hi : lo. Written as asm because the compiler would wait for every
-// such load before the next LDS read; the kernel counts them itself. No register is loaded. A
-// load whose mask is empty moves nothing and is counted like the others.
-__device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int lo, int hi) {
+// Loads of 64 lanes straight into LDS: 16 (4) bytes from each lane's address base + off to
+// consecutive LDS bytes at the wave-uniform address lds; the pair: two, 1024 LDS bytes apart
+// (the instruction's offset moves both addresses: base is 1024 low, o0 1024 high). Lanes outside hi : lo load
+// nothing, and a load with an empty mask is counted like the others. Written as asm because the
+// compiler would wait for every such load before the next LDS read; the kernel counts them
+// itself. No register is loaded.
+__device__ __forceinline__ void dma16_pair(const uint8_t *base, uint32_t o0, uint32_t o1, uint32_t lds, int lo, int hi) {
   asm volatile(
-      "s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1" ::"s"(
-          lds),
-      "v"(off), "s"(base), "s"(lo), "s"(hi)
+      "s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\t"
+      "global_load_lds_dwordx4 %3, %5\n\tglobal_load_lds_dwordx4 %4, %5 offset:1024\n\t"
+      "s_mov_b64 exec, -1" ::"s"(lds),
+      "s"(lo), "s"(hi), "v"(o0), "v"(o1), "s"(base)
       : "memory");
+}
+__device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int lo, int hi) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dwordx4 %3, %4\n\ts_mov_b64 exec, -1" ::"s"(lds),
+               "s"(lo), "s"(hi), "v"(off), "s"(base)
+               : "memory");
 }
 __device__ __forceinline__ void dma4(const uint8_t *base, uint32_t off, uint32_t lds, int lo, int hi) {
-  asm volatile(
-      "s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2\n\ts_mov_b64 exec, -1" ::"s"(
-          lds),
-      "v"(off), "s"(base), "s"(lo), "s"(hi)
-      : "memory");
-}
-__device__ __forceinline__ void dma16(uint64_t addr, uint32_t lds, int lo, int hi) {  // an address of each lane's own
-  asm volatile("s_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1" ::"s"(
-                   lds),
-               "v"(addr), "s"(lo), "s"(hi)
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dword %3, %4\n\ts_mov_b64 exec, -1" ::"s"(lds),
+               "s"(lo), "s"(hi), "v"(off), "s"(base)
                : "memory");
 }
 
@@ -35,41 +35,40 @@ __device__ __forceinline__ void wait_loads() {  // all but the last N loads of t
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int KB_, int NBUF_, int OCC_, bool WIDE_ = true>
+// BM x BN tile, WM x WN wavefronts, NBUF K stages of 8 blocks (256 inputs) in LDS, OCC workgroups per CU
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int OCC_, bool WIDE_ = true>
 struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;  // tile; wavefronts along its rows and columns
-  static constexpr int KB = KB_, KS = KB / 2;                   // blocks of a K stage, its K steps of 64 inputs
-  static constexpr int NBUF = NBUF_, OCC = OCC_;                // stages in LDS; workgroups per CU
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_, OCC = OCC_;
+  static constexpr int KB = 8, KS = 4;                          // blocks of a stage, its K steps of 64 inputs
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;    // 32 x 32 tiles of a wavefront
   static constexpr int ROWS = BM + BN;
-  static constexpr int RPL = 64 / KB;                           // rows of a 16-byte load (64 lanes)
-  static constexpr int LA = BM / 4 / RPL, LB = BN / 4 / RPL;    // 16-byte loads of a wavefront per stage
-  // Scales. WIDE: a window of 16 bytes of a row serves QN = 16 / KB stages (rows of 16 blocks or
-  // more); it is loaded in QN parts, one with each stage, and NSB windows are held. Else: the
-  // dwords of a stage with the stage.
+  static constexpr int LA = BM / 32, LB = BN / 32;              // 16-byte loads of a wavefront per stage (8 rows each)
+  // Scales. WIDE: a window of 16 bytes of a row serves two stages (rows of 16 blocks or more);
+  // it is loaded with the first (with the second its loads are empty) and NSB windows are held.
+  // Else: the two dwords of a stage with the stage.
   static constexpr bool WIDE = WIDE_;
-  static constexpr int QN = 16 / KB, RQ = ROWS / (4 * QN);      // parts of a window, rows of a wavefront in one
-  static constexpr int NSB = 2 + (NBUF - 2 + QN - 1) / QN;      // the window after next starts before this one ends
-  static constexpr int LR = (ROWS + 255) / 256, LS = WIDE ? 1 : LR * (KB / 4);
+  static constexpr int NSB = 1 + NBUF / 2;
+  static constexpr int RA = BM / 4, RB = BN / 4;                // scale rows of a wavefront
+  static constexpr int LS = WIDE ? 2 : 4;
   static constexpr int LOADS = LA + LB + LS;
-  static constexpr int STAGE = ROWS * KB * 16 + (WIDE ? 0 : LS * 1024);  // LDS bytes: codes, then planes of dwords
-  static constexpr int WINDOWS = NBUF * STAGE;                           // offset of the windows
-  static constexpr int BYTES = WINDOWS + (WIDE ? NSB * ROWS * 16 : 0);
+  static constexpr int STAGE = ROWS * (KB * 16 + (WIDE ? 0 : 8));  // LDS bytes: codes, then two planes of dwords
+  static constexpr int WINDOWS = NBUF * STAGE;                     // offset of the windows
+  static constexpr int IDS = WINDOWS + (WIDE ? NSB * ROWS * 16 : 0);  // offset of the row ids
+  static constexpr int BYTES = IDS + BM * 4;
+  static_assert(LA % 2 == 0 && LB % 2 == 0 && RA <= 64 && RB <= 64);
+  static_assert((NBUF - 1) * LOADS <= 63, "vmcnt");
 };
 
-template <int SA, int SB>
-__device__ __forceinline__ v16f mx_mfma32(uint4 a, uint32_t ua, uint4 b, uint32_t ub, v16f c) {
+template <int S>
+__device__ __forceinline__ v16f mx_mfma32(uint4 a, uint32_t ua, uint4 b, uint32_t ub, v16f c) {  // byte S of the scales
   const v8i32 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const v8i32 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SA, (int)ua, SB, (int)ub);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)ua, S, (int)ub);
 }
 
-// Slot of 16-byte chunk c of an LDS row of KB chunks is c ^ swizzle: the rows that one LDS
-// access reads at the same chunk fall on different banks.
-template <int KB>
-__device__ __forceinline__ int tile_swizzle(int row) {
-  return KB == 4 ? ((row >> 1) & 3) ^ ((row >> 3) & 1) : row & 7;
-}
+// Slot of chunk (block) c of an LDS row of eight is c ^ swizzle: the rows that one LDS access
+// reads at the same chunk fall on different banks.
+__device__ __forceinline__ int tile_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 // Workgroup id -> tile (x of nx, y of ny) of a dense product. Consecutive ids go to different
 // XCDs (id % 8); each XCD gets a run of tiles in strips of TILE_STRIP columns, so that the
@@ -88,21 +87,25 @@ template <MxMode MODE, typename T, typename S>
 __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int BM = S::BM, BN = S::BN, MI = S::MI, NI = S::NI, NBUF = S::NBUF, KB = S::KB, KS = S::KS;
+  constexpr int BF = MODE == MX_GATEUP ? BN / 2 : BN;  // output columns of a tile
+  static_assert(MODE != MX_GATEUP || NI % 2 == 0, "a wavefront holds gate and up columns");
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / S::WN, wn = wv % S::WN;
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, nst = (nb + KB - 1) / KB;
-  constexpr int BF = MODE == MX_GATEUP ? BN / 2 : BN;  // output columns of a tile
-  int bx = blockIdx.x, by = blockIdx.y;
-  if constexpr (MODE == MX_LINEAR) tile_of(blockIdx.x, (a.N + BF - 1) / BF, (a.M + BM - 1) / BM, bx, by);
-  const int n0 = bx * BF;
+  const int nx = (a.N + BF - 1) / BF;
 
-  // the rows of activations: first .. first + n - 1 of perm, or of the tokens
-  int e = 0, first = 0, n = 0;
+  // the rows of activations: first .. first + n - 1 of perm, or of the tokens; and the column
+  // tiles bx .. bx + cols - 1, one after another
+  int bx, by, cols, e = 0, first = 0, n = 0;
   bool routed = false;
   if constexpr (MODE == MX_LINEAR) {
+    tile_of(blockIdx.x, nx, (a.M + BM - 1) / BM, bx, by);
+    cols = 1;
     first = by * BM;
     n = min(BM, a.M - first);
   } else {
+    bx = blockIdx.x * a.strip, by = blockIdx.y;
+    cols = min(a.strip, nx - bx);
     if (by >= *a.ntiles) return;
     const int4 c = a.tiles[by];
     e = c.x;
@@ -111,198 +114,240 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     routed = c.w != 0;
   }
   const int64_t P = (int64_t)a.M * a.k;
-  auto act_row = [&](int i) -> int64_t {  // row of activations of tile row i
-    const int ci = first + min(i, n - 1);
-    if constexpr (MODE == MX_LINEAR) return ci;
-    const int64_t pair = routed ? a.perm[ci] : P + ci;
-    return MODE == MX_DOWN ? pair : (routed ? pair / a.k : ci);
+  // tile row i -> row of the output, of the activations
+  int *ids = reinterpret_cast<int *>(lds + S::IDS);
+  if constexpr (MODE != MX_LINEAR) {
+    for (int i = threadIdx.x; i < BM; i += 256) {
+      const int ci = first + min(i, n - 1);
+      ids[i] = routed ? a.perm[ci] : (int)(P + ci);
+    }
+    __syncthreads();
+  }
+  auto out_row = [&](int i) -> int64_t { return MODE == MX_LINEAR ? first + i : ids[i]; };
+  auto act_row = [&](int i) -> int {  // relative to the base below
+    if constexpr (MODE == MX_LINEAR) return min(i, n - 1);
+    return MODE == MX_DOWN ? ids[i] : (routed ? ids[i] / a.k : ids[i] - (int)P);
   };
-  auto w_row = [&](int r) -> int {  // weight row of tile column r
+  auto w_row = [&](int r) -> int {  // weight row of column r of the first tile, relative to the base below
     if constexpr (MODE == MX_GATEUP) {
       constexpr int WT = BN / S::WN;
       const int rr = r % WT, m = rr / (WT / 2);
-      return m * a.N + min(n0 + (r / WT) * (WT / 2) + rr % (WT / 2), a.N - 1);
+      return m * a.N + min((r / WT) * (WT / 2) + rr % (WT / 2), a.N - 1 - bx * BF);
     }
-    return min(n0 + r, a.N - 1);
+    return min(r, a.N - 1 - bx * BF);
   };
-  const uint8_t *wc = a.wc + (int64_t)e * a.wc_stride, *ws = a.ws + (int64_t)e * a.ws_stride;
   // tile-relative bases keep the lanes' offsets within 32 bits
-  const int wr0 = MODE == MX_GATEUP ? 0 : n0, ar0 = MODE == MX_LINEAR ? first : 0;
-  const uint8_t *ac = a.ac + (int64_t)ar0 * nbp * 16, *as = a.as + (int64_t)ar0 * nbp;
-  wc += (int64_t)wr0 * nb * 16;
-  ws += (int64_t)wr0 * a.ws_pitch;
+  const uint8_t *ac = a.ac, *as = a.as;
+  if constexpr (MODE == MX_LINEAR) ac += (int64_t)first * nbp * 16, as += (int64_t)first * nbp;
+  const uint8_t *wc = a.wc + (int64_t)e * a.wc_stride + (int64_t)bx * BF * nb * 16;
+  const uint8_t *ws = a.ws + (int64_t)e * a.ws_stride + (int64_t)bx * BF * a.ws_pitch;
 
-  // loads of this wavefront: RPL rows of KB chunks each; lane l: row l / KB, slot l % KB
-  constexpr int RPL = S::RPL;
-  const int lr = lane / KB, chunk = (lane % KB) ^ tile_swizzle<KB>(lr);
-  uint32_t oa[S::LA], ob[S::LB], os[S::LR];
-  uint64_t pw[S::QN];  // scale rows of this lane
+  // code loads of this wavefront: 8 rows of KB chunks each; lane l: row l / 8, slot l % 8. The
+  // swizzle's bit 3 of the row is the load's parity.
+  const int lr = lane >> 3, chunk = (lane & 7) ^ lr;
+  uint32_t oa[S::LA], ob[S::LB];
 #pragma unroll
-  for (int i = 0; i < S::LA; i++) oa[i] = (uint32_t)(act_row((wv * S::LA + i) * RPL + lr) - ar0) * (uint32_t)(nbp * 16) + chunk * 16;
+  for (int i = 0; i < S::LA; i++)
+    oa[i] = (uint32_t)act_row((wv * S::LA + i) * 8 + lr) * (uint32_t)(nbp * 16) + (chunk ^ (i & 1)) * 16 + (i & 1 ? 0 : 1024);
 #pragma unroll
-  for (int i = 0; i < S::LB; i++) ob[i] = (uint32_t)(w_row((wv * S::LB + i) * RPL + lr) - wr0) * (uint32_t)(nb * 16);
-  if constexpr (S::WIDE) {
-#pragma unroll
-    for (int q = 0; q < S::QN; q++) {
-      const int r = (q * 4 + wv) * S::RQ + min(lane, S::RQ - 1);
-      const uint8_t *p = r < BM ? as + (act_row(r) - ar0) * nbp : ws + (int64_t)(w_row(r - BM) - wr0) * a.ws_pitch;
-      pw[q] = reinterpret_cast<uint64_t>(p);
-    }
-  } else
-#pragma unroll
-  for (int i = 0; i < S::LR; i++) {
-    const int r = i * 256 + wv * 64 + lane;  // BM is a multiple of 64: a wavefront's rows are of one side
-    os[i] = r < BM ? (uint32_t)(act_row(r) - ar0) * (uint32_t)nbp
-                   : (uint32_t)(w_row(min(r, S::ROWS - 1) - BM) - wr0) * (uint32_t)a.ws_pitch;
-  }
+  for (int i = 0; i < S::LB; i++)
+    ob[i] = (uint32_t)w_row((wv * S::LB + i) * 8 + lr) * (uint32_t)(nb * 16) + (chunk ^ (i & 1)) * 16 + (i & 1 ? 0 : 1024);
+  // weight blocks past K repeat the row's last one: they meet activations of zero
+  const uint32_t past0 = max((nst - 1) * KB + chunk - (nb - 1), 0) * 16;
+  const uint32_t past1 = max((nst - 1) * KB + (chunk ^ 1) - (nb - 1), 0) * 16;
+  const int srow = min(lane, S::RA - 1), wrow = min(lane, S::RB - 1);
+  const uint32_t osa = (uint32_t)act_row(wv * S::RA + srow) * (uint32_t)nbp;
+  const uint32_t osb = (uint32_t)w_row(wv * S::RB + wrow) * (uint32_t)a.ws_pitch;
+  constexpr uint64_t LANES_A = ~0ull >> (64 - S::RA), LANES_B = ~0ull >> (64 - S::RB);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
   const int wlast = a.ws_pitch - 16;  // the last window ends with the row
-  auto window = [&](int u, int q, int on) {  // part q of scale window u
-    uint64_t p = pw[0];
-#pragma unroll
-    for (int i = 1; i < S::QN; i++) {
-      const uint64_t m = -(uint64_t)(q == i);  // (a select here becomes an array in memory)
-      p = (p & ~m) | (pw[i] & m);
-    }
-    const uint32_t dst = lds0 + S::WINDOWS + (u % S::NSB) * (S::ROWS * 16) + (q * 4 + wv) * (S::RQ * 16);
-    constexpr uint64_t lanes = ~0ull >> (64 - S::RQ);
-    dma16(p + min(16 * u, wlast), dst, on & (int)lanes, on & (int)(lanes >> 32));
+
+  // The loads run ahead of the products, over the stages of all column tiles: stage si of the
+  // tile whose weights start at pb, buffer slot, window counter.
+  int si = 0, slot = 0, win = 0, left = cols * nst;
+  const uint8_t *pb = wc, *psb = ws;
+  int on = -1;            // 0 once every stage is under way: the loads are empty
+  uint32_t past = 0;      // all ones at a row's last stage
+  auto issue_start = [&]() {
+    on = __builtin_amdgcn_readfirstlane(-left >> 31);
+    past = si == nst - 1 ? ~0u : 0u;
   };
-  // load q of stage s (an empty one past the last), into the buffer that stage s - NBUF had
-  auto issue = [&](int s, int q) {
-    const int on = __builtin_amdgcn_readfirstlane(s < nst ? -1 : 0);
-    const uint32_t buf = lds0 + (s % NBUF) * S::STAGE;
-    if (q < S::LA) {
-      dma16(ac + s * (KB * 16), oa[q], buf + (wv * S::LA + q) * 1024, on, on);
-    } else if (q < S::LA + S::LB) {
-      const int i = q - S::LA;
-      // weight blocks past K repeat the last one: they meet activations of zero
-      dma16(wc, ob[i] + min(s * KB + chunk, nb - 1) * 16, buf + BM * (KB * 16) + (wv * S::LB + i) * 1024, on, on);
+  auto issue = [&](int q) {  // load (of the codes: loads 2 q and 2 q + 1) q of the stage
+    const uint32_t buf = lds0 + slot * S::STAGE;
+    if (q < S::LA / 2) {
+      dma16_pair(ac + si * (KB * 16) - 1024, oa[2 * q], oa[2 * q + 1], buf + (wv * S::LA + 2 * q) * 1024, on, on);
+    } else if (q < (S::LA + S::LB) / 2) {
+      const int i = 2 * q - S::LA;
+      dma16_pair(pb + si * (KB * 16) - 1024, ob[i] - (past0 & past), ob[i + 1] - (past1 & past),
+                 buf + BM * (KB * 16) + (wv * S::LB + i) * 1024, on, on);
     } else if constexpr (S::WIDE) {
-      window((s + S::QN - 1) / S::QN, (s + S::QN - 1) % S::QN, on);  // stage 0 completes window 0
+      const uint32_t dst = lds0 + S::WINDOWS + win * (S::ROWS * 16);
+      const int at = min(si * KB, wlast);
+      const int fresh = on & ((si & 1) - 1);  // the first of the window's two stages
+      if (q == (S::LA + S::LB) / 2)
+        dma16(as + at, osa, dst + wv * (S::RA * 16), fresh & (int)LANES_A, fresh & (int)(LANES_A >> 32));
+      else
+        dma16(psb + at, osb, dst + (BM + wv * S::RB) * 16, fresh & (int)LANES_B, fresh & (int)(LANES_B >> 32));
     } else {
-      const int i = (q - S::LA - S::LB) % S::LR, d = (q - S::LA - S::LB) / S::LR, r0 = i * 256 + wv * 64;
-      // a dword past the row's scales is replaced by its last: nb is a multiple of 4 or the rows are padded
-      const int b = r0 < BM ? s * KB + 4 * d : min(s * KB + 4 * d, a.ws_pitch - 4);
-      dma4((r0 < BM ? as : ws) + b, os[i], buf + S::ROWS * (KB * 16) + d * (S::LR * 1024) + r0 * 4, on, on);
+      const int i = q - (S::LA + S::LB) / 2, d = i & 1;
+      const uint32_t dst = buf + S::ROWS * (KB * 16) + d * (S::ROWS * 4);
+      // a dword past the row's scales is replaced by its last
+      if (i < 2)
+        dma4(as + si * KB + 4 * d, osa, dst + wv * (S::RA * 4), on & (int)LANES_A, on & (int)(LANES_A >> 32));
+      else
+        dma4(psb + min(si * KB + 4 * d, a.ws_pitch - 4), osb, dst + (BM + wv * S::RB) * 4, on & (int)LANES_B, on & (int)(LANES_B >> 32));
+    }
+  };
+  constexpr int ISSUES = (S::LA + S::LB) / 2 + S::LS;
+  auto issue_end = [&]() {
+    slot = slot == NBUF - 1 ? 0 : slot + 1;
+    left--;
+    si++;
+    const bool wrap = si == nst;
+    if ((si & 1) == 0 || wrap) win = win == S::NSB - 1 ? 0 : win + 1;
+    if (wrap) {
+      si = 0;
+      pb += (int64_t)BF * nb * 16;
+      psb += (int64_t)BF * a.ws_pitch;
     }
   };
 
-  v16f acc[MI][NI] = {};
+  v16f acc[MI][NI];
   const int li = lane & 31, hh = lane >> 5;
-  const int ra = wm * (BM / S::WM) + li, rb = wn * (BN / S::WN) + li;
+  // K step t takes block t of a stage in lanes 0-31 and block 4 + t in lanes 32-63, so that a
+  // lane's scales are the four bytes of one dword
+  uint32_t ra[KS], rb[KS];
+#pragma unroll
+  for (int t = 0; t < KS; t++) {
+    const int c = ((t + 4 * hh) ^ tile_swizzle(li)) * 16;
+    ra[t] = (wm * (BM / S::WM) + li) * (KB * 16) + c;
+    rb[t] = (BM + wn * (BN / S::WN) + li) * (KB * 16) + c;
+  }
   uint4 fa[2][MI], fb[2][NI];
-  uint32_t sa[KB / 4][MI], sb[KB / 4][NI], sa_next[KB / 4][MI], sb_next[KB / 4][NI];
-  auto read = [&](int s, int t) {  // fragments of K step t of stage s
-    const uint8_t *buf = lds + (s % NBUF) * S::STAGE;
-    const int c = ((2 * t + hh) ^ tile_swizzle<KB>(li)) * 16;
-#pragma unroll
-    for (int i = 0; i < MI; i++) fa[t & 1][i] = *reinterpret_cast<const uint4 *>(buf + (ra + i * 32) * (KB * 16) + c);
-#pragma unroll
-    for (int j = 0; j < NI; j++)
-      fb[t & 1][j] = *reinterpret_cast<const uint4 *>(buf + (BM + rb + j * 32) * (KB * 16) + c);
+  uint32_t sa[2][MI], sb[2][NI];
+  auto read = [&](int slot, int t, int p) {  // fragment p (rows', then columns') of K step t of a stage
+    const uint8_t *buf = lds + slot * S::STAGE;
+    if (p < MI)
+      fa[t & 1][p] = *reinterpret_cast<const uint4 *>(buf + ra[t] + p * (32 * KB * 16));
+    else
+      fb[t & 1][p - MI] = *reinterpret_cast<const uint4 *>(buf + rb[t] + (p - MI) * (32 * KB * 16));
   };
-  auto read_scales = [&](int s) {  // a dword: four blocks of a row
+  auto read_scales = [&](int slot, int win, int s) {
+    const uint8_t *p;
+    constexpr int step = S::WIDE ? 16 : 4;  // bytes between rows
+    if constexpr (S::WIDE)  // the lane's dword of the window; past the row's end: the last one
+      p = lds + S::WINDOWS + win * (S::ROWS * 16) + min(s * KB - min(s / 2 * 16, wlast) + 4 * hh, 12);
+    else
+      p = lds + slot * S::STAGE + S::ROWS * (KB * 16) + hh * (S::ROWS * 4);
+    p += (wm * (BM / S::WM) + li) * step;
 #pragma unroll
-    for (int d = 0; d < KB / 4; d++) {
-      const uint8_t *p;
-      constexpr int step = S::WIDE ? 16 : 4;  // bytes between rows
-      if constexpr (S::WIDE) {
-        const int u = s / S::QN, at = s * KB + 4 * d - min(16 * u, wlast);  // past the row's end: its last dword
-        p = lds + S::WINDOWS + (u % S::NSB) * (S::ROWS * 16) + min(at, 12);
-      } else {
-        p = lds + (s % NBUF) * S::STAGE + S::ROWS * (KB * 16) + d * (S::LR * 1024);
-      }
+    for (int i = 0; i < MI; i++) sa[1][i] = *reinterpret_cast<const uint32_t *>(p + i * 32 * step);
+    p += (BM + wn * (BN / S::WN) - wm * (BM / S::WM)) * step;
 #pragma unroll
-      for (int i = 0; i < MI; i++) sa_next[d][i] = *reinterpret_cast<const uint32_t *>(p + (ra + i * 32) * step);
-#pragma unroll
-      for (int j = 0; j < NI; j++) sb_next[d][j] = *reinterpret_cast<const uint32_t *>(p + (BM + rb + j * 32) * step);
-    }
+    for (int j = 0; j < NI; j++) sb[1][j] = *reinterpret_cast<const uint32_t *>(p + j * 32 * step);
   };
-  auto take_scales = [&]() {  // bytes 0 and 2: this lane's blocks of two K steps
+  auto take_scales = [&]() {
 #pragma unroll
-    for (int d = 0; d < KB / 4; d++) {
+    for (int i = 0; i < MI; i++) sa[0][i] = sa[1][i];
 #pragma unroll
-      for (int i = 0; i < MI; i++) sa[d][i] = sa_next[d][i] >> (8 * hh);
-#pragma unroll
-      for (int j = 0; j < NI; j++) sb[d][j] = sb_next[d][j] >> (8 * hh);
-    }
+    for (int j = 0; j < NI; j++) sb[0][j] = sb[1][j];
   };
   auto mul = [&](int t, int i, int j) {
-    acc[i][j] = t & 1 ? mx_mfma32<2, 2>(fa[1][i], sa[t / 2][i], fb[1][j], sb[t / 2][j], acc[i][j])
-                      : mx_mfma32<0, 0>(fa[0][i], sa[t / 2][i], fb[0][j], sb[t / 2][j], acc[i][j]);
+    const uint4 x = fa[t & 1][i], y = fb[t & 1][j];
+    const uint32_t u = sa[0][i], v = sb[0][j];
+    acc[i][j] = t == 0 ? mx_mfma32<0>(x, u, y, v, acc[i][j]) : t == 1 ? mx_mfma32<1>(x, u, y, v, acc[i][j])
+              : t == 2 ? mx_mfma32<2>(x, u, y, v, acc[i][j]) : mx_mfma32<3>(x, u, y, v, acc[i][j]);
   };
 
-  // Stages s + 1 .. s + NBUF - 1 are on their way while stage s is multiplied. A stage's last K
-  // step is in registers before its buffer is given up, and is multiplied while the loads of
-  // stage s + NBUF and the first fragments of stage s + 1 are under way. The body has no branch:
-  // the compiler would move products across it, behind the wait.
-  if constexpr (S::WIDE)
+  // While a stage is multiplied the NBUF - 1 after it are on their way. Its last K step is in
+  // registers before its buffer is given up, and is multiplied while the loads of stage + NBUF
+  // and the first fragments of the next stage are under way. The products' part of the body
+  // has no branch: the compiler would move products across it, behind the wait.
 #pragma unroll
-    for (int q = 0; q < S::QN - 1; q++) window(0, q, -1);
+  for (int s = 0; s < NBUF; s++) {
+    issue_start();
 #pragma unroll
-  for (int s = 0; s < NBUF; s++)
-#pragma unroll
-    for (int q = 0; q < S::LOADS; q++) issue(s, q);
-  static_assert((NBUF - 1) * S::LOADS <= 63, "vmcnt");
+    for (int q = 0; q < ISSUES; q++) issue(q);
+    issue_end();
+  }
   wait_loads<(NBUF - 1) * S::LOADS>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  read_scales(0);
-  read(0, 0);
+  int cur = 0, cwin = 0;  // buffer slot and window of the stage that is multiplied
+  read_scales(0, 0, 0);
+#pragma unroll
+  for (int p = 0; p < MI + NI; p++) read(0, 0, p);
   take_scales();
-  for (int s = 0; s < nst; s++) {
+  for (int col = 0; col < cols; col++) {
 #pragma unroll
-    for (int t = 0; t < KS - 1; t++) {
-      read(s, t + 1);
+    for (int i = 0; i < MI; i++)
 #pragma unroll
-      for (int q = 0; q < MI * NI; q++) mul(t, q / NI, q % NI);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    wait_loads<(NBUF - 2) * S::LOADS>();  // stage s + 1 has arrived; stage s is in registers
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    // products and loads take turns: a burst of loads would leave the matrix cores without work
-    constexpr int TURNS = MI * NI > 3 ? MI * NI : 3, PER = (S::LOADS + TURNS - 3) / (TURNS - 2);
+      for (int j = 0; j < NI; j++) acc[i][j] = v16f{};
+    for (int s = 0; s < nst; s++) {
+      // products, fragment reads and loads take turns, in this order: the next step's fragments
+      // are read early in a step, and a burst of loads would leave the matrix cores without work
+      constexpr int MUL = MI * NI, RT = (MUL + 1) / 2, RP = (MI + NI + RT - 1) / RT;
 #pragma unroll
-    for (int q = 0; q < TURNS; q++) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (q < MI * NI) mul(KS - 1, q / NI, q % NI);
-      if (q == 0) read_scales(s + 1);  // past the last stage: not used
-      if (q == 1) read(s + 1, 0);
+      for (int t = 0; t < KS - 1; t++)
 #pragma unroll
-      for (int p = (q - 2) * PER; p < (q - 1) * PER; p++)
-        if (p >= 0 && p < S::LOADS) issue(s + NBUF, p);
-    }
-    take_scales();
-  }
-
-  // results: lane column li of a tile, rows 8 (r / 4) + 4 hh + r % 4
+        for (int q = 0; q < MUL; q++) {
+          mul(t, q / NI, q % NI);
 #pragma unroll
-  for (int i = 0; i < MI; i++)
-#pragma unroll
-    for (int r = 0; r < 16; r++) {
-      const int row = wm * (BM / S::WM) + i * 32 + 8 * (r / 4) + 4 * hh + (r & 3);
-      if (row >= n) continue;
-      const int ci = first + row;
-      const int64_t orow = MODE == MX_LINEAR ? ci : (routed ? (int64_t)a.perm[ci] : P + ci);
-      if constexpr (MODE == MX_GATEUP) {
-#pragma unroll
-        for (int j = 0; j < NI / 2; j++) {
-          const int col = n0 + wn * (BN / S::WN / 2) + j * 32 + li;
-          if (col < a.N) static_cast<T *>(a.out)[orow * a.N + col] = (T)(silu(acc[i][j][r]) * acc[i][j + NI / 2][r]);
+          for (int p = q * RP; p < (q + 1) * RP && p < MI + NI; p++) read(cur, t + 1, p);
+          __builtin_amdgcn_sched_barrier(0);
         }
-      } else {
+      const bool last = s == nst - 1;
+      const int next = cur == NBUF - 1 ? 0 : cur + 1, ns = last ? 0 : s + 1;
+      if ((s & 1) || last) cwin = cwin == S::NSB - 1 ? 0 : cwin + 1;
+      issue_start();
+      wait_loads<(NBUF - 2) * S::LOADS>();  // the next stage has arrived; this one is in registers
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      constexpr int PER = (ISSUES + MUL - 1) / MUL;
 #pragma unroll
-        for (int j = 0; j < NI; j++) {
-          const int col = n0 + wn * (BN / S::WN) + j * 32 + li;
-          if (col < a.N) static_cast<T *>(a.out)[orow * a.N + col] = (T)acc[i][j][r];
+      for (int q = 0; q < MUL; q++) {
+        __builtin_amdgcn_sched_barrier(0);
+        mul(KS - 1, q / NI, q % NI);
+        if (q == 0) read_scales(next, cwin, ns);  // past the last stage: not used
+#pragma unroll
+        for (int p = q * PER; p < (q + 1) * PER && p < ISSUES; p++) issue(p);
+#pragma unroll
+        for (int p = q * RP; p < (q + 1) * RP && p < MI + NI; p++) read(next, 0, p);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      issue_end();
+      take_scales();
+      cur = next;
+    }
+    // results: lane column li of a 32 x 32 tile, rows 8 (r / 4) + 4 hh + r % 4
+#pragma unroll
+    for (int i = 0; i < MI; i++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) {
+        const int row = wm * (BM / S::WM) + i * 32 + 8 * (r / 4) + 4 * hh + (r & 3);
+        const int64_t o = out_row(row) * a.N + (bx + col) * BF;
+        const int nleft = row < n ? a.N - (bx + col) * BF : 0;  // columns that exist
+        if constexpr (MODE == MX_GATEUP) {
+#pragma unroll
+          for (int j = 0; j < NI / 2; j++) {
+            const int c = wn * (BN / S::WN / 2) + j * 32 + li;
+            if (c < nleft) static_cast<T *>(a.out)[o + c] = (T)(silu(acc[i][j][r]) * acc[i][j + NI / 2][r]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NI; j++) {
+            const int c = wn * (BN / S::WN) + j * 32 + li;
+            if (c < nleft) static_cast<T *>(a.out)[o + c] = (T)acc[i][j][r];
+          }
         }
       }
-    }
+  }
 }
 
+#ifndef STRIP
+#define STRIP 2
+#endif
 // Tiles of a route: {expert, first (of perm, or token), rows, routed}, the shared expert's first.
 __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap) {
   __shared__ int wsum[16];
@@ -337,24 +382,25 @@ __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap
 }
 
 template <MxMode MODE, typename T, typename S>
-static hipError_t launch_tile(const MxArgs &a, int ny, hipStream_t s) {
+static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static_assert(S::BYTES <= 160 * 1024, "LDS");
   constexpr int BF = MODE == MX_GATEUP ? S::BN / 2 : S::BN;
   auto kernel = mx_tile_kernel<MODE, T, S>;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (attr != hipSuccess) return attr;
-  const unsigned nx = (unsigned)((a.N + BF - 1) / BF);
-  const dim3 g = MODE == MX_LINEAR ? dim3(nx * (unsigned)ny) : dim3(nx, (unsigned)ny);
+  const int nx = (a.N + BF - 1) / BF;
+  a.strip = STRIP;
+  const dim3 g = MODE == MX_LINEAR ? dim3((unsigned)(nx * ny)) : dim3((unsigned)((nx + a.strip - 1) / a.strip), (unsigned)ny);
   hipLaunchKernelGGL(kernel, g, dim3(256), S::BYTES, s, a);
   return hipGetLastError();
 }
 
 #ifndef TD
-#define TD 256, 256, 2, 2, 4, 4, 1
+#define TD 256, 256, 2, 2, 2, 1
 #endif
 #ifndef TE
-#define TE 128, 256, 1, 4, 4, 4, 1
+#define TE 128, 256, 2, 2, 3, 1
 #endif
 typedef TileShape<TD> TileDense;
 typedef TileShape<TE> TileExperts;

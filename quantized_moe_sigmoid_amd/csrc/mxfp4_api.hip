@@ -44,7 +44,7 @@ static MxWs mx_ws_linear(int32_t M, int32_t N, int32_t K) {
 
 static int check_linear(int32_t M, int32_t N, int32_t K) {
   if (M < 0 || N < 0 || K <= 0) return COLI_E_INVALID;
-  if (K % 32 || K > (1 << 20) || M > (1 << 20) || N > (1 << 24)) return COLI_E_UNSUPPORTED;
+  if (K % 32 || K > (1 << 20) || M > (1 << 20) || N > (1 << 20)) return COLI_E_UNSUPPORTED;
   return COLI_OK;
 }
 

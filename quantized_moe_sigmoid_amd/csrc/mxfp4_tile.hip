@@ -1,21 +1,23 @@
 // mxfp4_tile.hip — MXFP4 x MXFP4 products of many rows: LDS-tiled GEMMs on the scaled
 // 32x32x64 matrix instruction of gfx950, dense and grouped over a route (batch-union:
 // colibri-strix README, "What's implemented").
+#include <type_traits>
+
 #include "mxfp4_impl.h"
 
 namespace coli {
 
 // Loads of 64 lanes straight into LDS: 16 (4) bytes from each lane's address base + off to
-// consecutive LDS bytes at the wave-uniform address lds; the pair: two, 1024 LDS bytes apart
-// (the instruction's offset moves both addresses: base is 1024 low, o0 1024 high). Lanes outside hi : lo load
-// nothing, and a load with an empty mask is counted like the others. Written as asm because the
-// compiler would wait for every such load before the next LDS read; the kernel counts them
+// consecutive LDS bytes at the wave-uniform address lds; the pair: two, 4096 LDS bytes apart
+// (the instruction's offset moves both addresses, so o0 is 4096 high). Lanes outside hi : lo
+// load nothing, and a load with an empty mask is counted like the others. Written as asm because
+// the compiler would wait for every such load before the next LDS read; the kernel counts them
 // itself. No register is loaded.
 __device__ __forceinline__ void dma16_pair(const uint8_t *base, uint32_t o0, uint32_t o1, uint32_t lds, int lo, int hi) {
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\t"
-      "global_load_lds_dwordx4 %3, %5\n\tglobal_load_lds_dwordx4 %4, %5 offset:1024\n\t"
-      "s_mov_b64 exec, -1" ::"s"(lds),
+      "global_load_lds_dwordx4 %3, %5 offset:-4096\n\tglobal_load_lds_dwordx4 %4, %5\n\t"
+      "s_mov_b64 exec, -1" ::"s"(lds + 4096),
       "s"(lo), "s"(hi), "v"(o0), "v"(o1), "s"(base)
       : "memory");
 }
@@ -50,14 +52,15 @@ struct TileShape {
   static constexpr int NSB = 1 + NBUF / 2;
   static constexpr int RA = BM / 4, RB = BN / 4;                // scale rows of a wavefront
   static constexpr int LS = WIDE ? 2 : 4;
-  static constexpr int LOADS = LA + LB + LS;
   static constexpr int STAGE = ROWS * (KB * 16 + (WIDE ? 0 : 8));  // LDS bytes: codes, then two planes of dwords
   static constexpr int WINDOWS = NBUF * STAGE;                     // offset of the windows
   static constexpr int IDS = WINDOWS + (WIDE ? NSB * ROWS * 16 : 0);  // offset of the row ids
   static constexpr int BYTES = IDS + BM * 4;
-  static_assert(LA % 2 == 0 && LB % 2 == 0 && RA <= 64 && RB <= 64);
-  static_assert((NBUF - 1) * LOADS <= 63, "vmcnt");
+  static_assert(LB % 2 == 0 && RA <= 64 && RB <= 64);
 };
+
+typedef uint32_t v2u32 __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u32 __attribute__((ext_vector_type(4)));
 
 template <int S>
 __device__ __forceinline__ v16f mx_mfma32(uint4 a, uint32_t ua, uint4 b, uint32_t ub, v16f c) {  // byte S of the scales
@@ -83,7 +86,47 @@ __device__ __forceinline__ void tile_of(int id, int nx, int ny, int &x, int &y) 
   x = strip * TILE_STRIP + in - y * w;
 }
 
-template <MxMode MODE, typename T, typename S>
+// v: four rows of this lane's column -> row q (the lane's place in its quad) of the quad's four
+// columns, rounded to T
+template <typename T>
+__device__ __forceinline__ auto quad_transpose(const float (&v)[4], int q) {
+  auto swap = [](auto x, auto ctrl) {
+    return __builtin_bit_cast(decltype(x), __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  const bool odd = q & 1, up = q & 2;
+  const float s0 = swap(odd ? v[0] : v[1], std::integral_constant<int, 0xB1>{});  // lane ^ 1
+  const float s1 = swap(odd ? v[2] : v[3], std::integral_constant<int, 0xB1>{});
+  typedef T t2 __attribute__((ext_vector_type(2)));
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  // rows q % 2 and 2 + q % 2 of the columns of lanes q & 2, (q & 2) + 1
+  const t2 lo = {(T)(odd ? s0 : v[0]), (T)(odd ? v[1] : s0)};
+  const t2 hi = {(T)(odd ? s1 : v[2]), (T)(odd ? v[3] : s1)};
+  const t2 give = up ? lo : hi, keep = up ? hi : lo;
+  t2 got;
+  if constexpr (sizeof(T) == 2) {
+    got = swap(give, std::integral_constant<int, 0x4E>{});  // lane ^ 2
+  } else {
+    got[0] = swap(give[0], std::integral_constant<int, 0x4E>{});
+    got[1] = swap(give[1], std::integral_constant<int, 0x4E>{});
+  }
+  const t2 l = up ? got : keep, h = up ? keep : got;
+  return t4{l[0], l[1], h[0], h[1]};
+}
+
+template <typename W>
+__device__ __forceinline__ void store_out(W w, __amdgpu_buffer_rsrc_t out, uint32_t off) {
+  if constexpr (sizeof(W) == 16)
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, w), out, off, 0, 0);
+  else if constexpr (sizeof(W) == 8)
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, w), out, off, 0, 0);
+  else if constexpr (sizeof(W) == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, w), out, off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, w), out, off, 0, 0);
+}
+
+// VEC: N is a multiple of 4
+template <MxMode MODE, typename T, typename S, bool VEC>
 __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int BM = S::BM, BN = S::BN, MI = S::MI, NI = S::NI, NBUF = S::NBUF, KB = S::KB, KS = S::KS;
@@ -99,8 +142,9 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   int bx, by, cols, e = 0, first = 0, n = 0;
   bool routed = false;
   if constexpr (MODE == MX_LINEAR) {
-    tile_of(blockIdx.x, nx, (a.M + BM - 1) / BM, bx, by);
-    cols = 1;
+    tile_of(blockIdx.x, (nx + a.strip - 1) / a.strip, (a.M + BM - 1) / BM, bx, by);
+    bx *= a.strip;
+    cols = min(a.strip, nx - bx);
     first = by * BM;
     n = min(BM, a.M - first);
   } else {
@@ -123,7 +167,12 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     }
     __syncthreads();
   }
-  auto out_row = [&](int i) -> int64_t { return MODE == MX_LINEAR ? first + i : ids[i]; };
+  auto out_row = [&](int i) -> int { return MODE == MX_LINEAR ? i : ids[i]; };  // relative to the buffer below
+  // the output from its first row on (of a dense product: the tile's); offsets fit in 32 bits
+  const int64_t rows = MODE == MX_LINEAR ? n : P + (a.has_shared ? a.M : 0);
+  const auto out = __builtin_amdgcn_make_buffer_rsrc(
+      static_cast<T *>(a.out) + (MODE == MX_LINEAR ? (int64_t)first * a.N : 0), 0, (int)(uint32_t)(rows * a.N * sizeof(T)),
+      0x00027000);
   auto act_row = [&](int i) -> int {  // relative to the base below
     if constexpr (MODE == MX_LINEAR) return min(i, n - 1);
     return MODE == MX_DOWN ? ids[i] : (routed ? ids[i] / a.k : ids[i] - (int)P);
@@ -142,19 +191,17 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   const uint8_t *wc = a.wc + (int64_t)e * a.wc_stride + (int64_t)bx * BF * nb * 16;
   const uint8_t *ws = a.ws + (int64_t)e * a.ws_stride + (int64_t)bx * BF * a.ws_pitch;
 
-  // code loads of this wavefront: 8 rows of KB chunks each; lane l: row l / 8, slot l % 8. The
-  // swizzle's bit 3 of the row is the load's parity.
-  const int lr = lane >> 3, chunk = (lane & 7) ^ lr;
+  // code load i of this wavefront: rows (4 i + wv) 8 .. + 7; lane l: row l / 8, slot l % 8
+  const int lr = lane >> 3, chunk = (lane & 7) ^ tile_swizzle(8 * wv + lr);
   uint32_t oa[S::LA], ob[S::LB];
 #pragma unroll
   for (int i = 0; i < S::LA; i++)
-    oa[i] = (uint32_t)act_row((wv * S::LA + i) * 8 + lr) * (uint32_t)(nbp * 16) + (chunk ^ (i & 1)) * 16 + (i & 1 ? 0 : 1024);
+    oa[i] = (uint32_t)act_row((4 * i + wv) * 8 + lr) * (uint32_t)(nbp * 16) + chunk * 16 + (i & 1 ? 0 : 4096);
 #pragma unroll
   for (int i = 0; i < S::LB; i++)
-    ob[i] = (uint32_t)w_row((wv * S::LB + i) * 8 + lr) * (uint32_t)(nb * 16) + (chunk ^ (i & 1)) * 16 + (i & 1 ? 0 : 1024);
+    ob[i] = (uint32_t)w_row((4 * i + wv) * 8 + lr) * (uint32_t)(nb * 16) + chunk * 16 + (i & 1 ? 0 : 4096);
   // weight blocks past K repeat the row's last one: they meet activations of zero
-  const uint32_t past0 = max((nst - 1) * KB + chunk - (nb - 1), 0) * 16;
-  const uint32_t past1 = max((nst - 1) * KB + (chunk ^ 1) - (nb - 1), 0) * 16;
+  const uint32_t past_k = max((nst - 1) * KB + chunk - (nb - 1), 0) * 16;
   const int srow = min(lane, S::RA - 1), wrow = min(lane, S::RB - 1);
   const uint32_t osa = (uint32_t)act_row(wv * S::RA + srow) * (uint32_t)nbp;
   const uint32_t osb = (uint32_t)w_row(wv * S::RB + wrow) * (uint32_t)a.ws_pitch;
@@ -162,186 +209,221 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
   const int wlast = a.ws_pitch - 16;  // the last window ends with the row
 
-  // The loads run ahead of the products, over the stages of all column tiles: stage si of the
-  // tile whose weights start at pb, buffer slot, window counter.
-  int si = 0, slot = 0, win = 0, left = cols * nst;
-  const uint8_t *pb = wc, *psb = ws;
-  int on = -1;            // 0 once every stage is under way: the loads are empty
-  uint32_t past = 0;      // all ones at a row's last stage
-  auto issue_start = [&]() {
-    on = __builtin_amdgcn_readfirstlane(-left >> 31);
-    past = si == nst - 1 ? ~0u : 0u;
-  };
-  auto issue = [&](int q) {  // load (of the codes: loads 2 q and 2 q + 1) q of the stage
-    const uint32_t buf = lds0 + slot * S::STAGE;
-    if (q < S::LA / 2) {
-      dma16_pair(ac + si * (KB * 16) - 1024, oa[2 * q], oa[2 * q + 1], buf + (wv * S::LA + 2 * q) * 1024, on, on);
-    } else if (q < (S::LA + S::LB) / 2) {
-      const int i = 2 * q - S::LA;
-      dma16_pair(pb + si * (KB * 16) - 1024, ob[i] - (past0 & past), ob[i + 1] - (past1 & past),
-                 buf + BM * (KB * 16) + (wv * S::LB + i) * 1024, on, on);
-    } else if constexpr (S::WIDE) {
-      const uint32_t dst = lds0 + S::WINDOWS + win * (S::ROWS * 16);
-      const int at = min(si * KB, wlast);
-      const int fresh = on & ((si & 1) - 1);  // the first of the window's two stages
-      if (q == (S::LA + S::LB) / 2)
-        dma16(as + at, osa, dst + wv * (S::RA * 16), fresh & (int)LANES_A, fresh & (int)(LANES_A >> 32));
-      else
-        dma16(psb + at, osb, dst + (BM + wv * S::RB) * 16, fresh & (int)LANES_B, fresh & (int)(LANES_B >> 32));
-    } else {
-      const int i = q - (S::LA + S::LB) / 2, d = i & 1;
-      const uint32_t dst = buf + S::ROWS * (KB * 16) + d * (S::ROWS * 4);
-      // a dword past the row's scales is replaced by its last
-      if (i < 2)
-        dma4(as + si * KB + 4 * d, osa, dst + wv * (S::RA * 4), on & (int)LANES_A, on & (int)(LANES_A >> 32));
-      else
-        dma4(psb + min(si * KB + 4 * d, a.ws_pitch - 4), osb, dst + (BM + wv * S::RB) * 4, on & (int)LANES_B, on & (int)(LANES_B >> 32));
-    }
-  };
-  constexpr int ISSUES = (S::LA + S::LB) / 2 + S::LS;
-  auto issue_end = [&]() {
-    slot = slot == NBUF - 1 ? 0 : slot + 1;
-    left--;
-    si++;
-    const bool wrap = si == nst;
-    if ((si & 1) == 0 || wrap) win = win == S::NSB - 1 ? 0 : win + 1;
-    if (wrap) {
-      si = 0;
-      pb += (int64_t)BF * nb * 16;
-      psb += (int64_t)BF * a.ws_pitch;
-    }
-  };
+  auto run = [&]<int MX>() {  // with MX 32-row tiles to a wavefront
+    // The loads run ahead of the products, over the stages of all column tiles: stage si of the
+    // tile whose weights start at pb, buffer slot, window counter.
+    int si = 0, slot = 0, win = 0, left = cols * nst;
+    const uint8_t *pb = wc, *psb = ws;
+    int on = -1;            // 0 once every stage is under way: the loads are empty
+    uint32_t past = 0;      // past_k at a row's last stage
+    auto issue_start = [&]() {
+      on = __builtin_amdgcn_readfirstlane(-left >> 31);
+      past = si == nst - 1 ? past_k : 0u;
+    };
+    constexpr int NA = S::WM == 1 ? MX : S::LA, QA = (NA + 1) / 2, QB = S::LB / 2;  // the codes' loads go in pairs; an odd one alone
+    auto issue = [&](int q) {  // load or pair q of the stage
+      const uint32_t buf = lds0 + slot * S::STAGE;
+      if (q < QA) {
+        const uint32_t dst = buf + (8 * q + wv) * 1024;
+        if (2 * q + 1 < NA)
+          dma16_pair(ac + si * (KB * 16), oa[2 * q], oa[2 * q + 1], dst, on, on);
+        else
+          dma16(ac + si * (KB * 16) - 4096, oa[2 * q], dst, on, on);
+      } else if (q < QA + QB) {
+        const int i = q - QA;
+        dma16_pair(pb + si * (KB * 16), ob[2 * i] - past, ob[2 * i + 1] - past,
+                   buf + BM * (KB * 16) + (8 * i + wv) * 1024, on, on);
+      } else if constexpr (S::WIDE) {
+        const uint32_t dst = lds0 + S::WINDOWS + win * (S::ROWS * 16);
+        const int at = min(si * KB, wlast);
+        const int fresh = on & ((si & 1) - 1);  // the first of the window's two stages
+        if (q == QA + QB)
+          dma16(as + at, osa, dst + wv * (S::RA * 16), fresh & (int)LANES_A, fresh & (int)(LANES_A >> 32));
+        else
+          dma16(psb + at, osb, dst + (BM + wv * S::RB) * 16, fresh & (int)LANES_B, fresh & (int)(LANES_B >> 32));
+      } else {
+        const int i = q - QA - QB, d = i & 1;
+        const uint32_t dst = buf + S::ROWS * (KB * 16) + d * (S::ROWS * 4);
+        // a dword past the row's scales is replaced by its last
+        if (i < 2)
+          dma4(as + si * KB + 4 * d, osa, dst + wv * (S::RA * 4), on & (int)LANES_A, on & (int)(LANES_A >> 32));
+        else
+          dma4(psb + min(si * KB + 4 * d, a.ws_pitch - 4), osb, dst + (BM + wv * S::RB) * 4, on & (int)LANES_B, on & (int)(LANES_B >> 32));
+      }
+    };
+    constexpr int ISSUES = QA + QB + S::LS, LOADS = NA + S::LB + S::LS;
+    static_assert((NBUF - 1) * LOADS <= 63, "vmcnt");
+    auto issue_end = [&]() {
+      slot = slot == NBUF - 1 ? 0 : slot + 1;
+      left--;
+      si++;
+      const bool wrap = si == nst;
+      if ((si & 1) == 0 || wrap) win = win == S::NSB - 1 ? 0 : win + 1;
+      if (wrap) {
+        si = 0;
+        pb += (int64_t)BF * nb * 16;
+        psb += (int64_t)BF * a.ws_pitch;
+      }
+    };
 
-  v16f acc[MI][NI];
-  const int li = lane & 31, hh = lane >> 5;
-  // K step t takes block t of a stage in lanes 0-31 and block 4 + t in lanes 32-63, so that a
-  // lane's scales are the four bytes of one dword
-  uint32_t ra[KS], rb[KS];
+    v16f acc[MX][NI];
+    const int li = lane & 31, hh = lane >> 5;
+    // K step t takes block t of a stage in lanes 0-31 and block 4 + t in lanes 32-63, so that a
+    // lane's scales are the four bytes of one dword
+    uint32_t ra[KS], rb[KS];
 #pragma unroll
-  for (int t = 0; t < KS; t++) {
-    const int c = ((t + 4 * hh) ^ tile_swizzle(li)) * 16;
-    ra[t] = (wm * (BM / S::WM) + li) * (KB * 16) + c;
-    rb[t] = (BM + wn * (BN / S::WN) + li) * (KB * 16) + c;
-  }
-  uint4 fa[2][MI], fb[2][NI];
-  uint32_t sa[2][MI], sb[2][NI];
-  auto read = [&](int slot, int t, int p) {  // fragment p (rows', then columns') of K step t of a stage
-    const uint8_t *buf = lds + slot * S::STAGE;
-    if (p < MI)
-      fa[t & 1][p] = *reinterpret_cast<const uint4 *>(buf + ra[t] + p * (32 * KB * 16));
-    else
-      fb[t & 1][p - MI] = *reinterpret_cast<const uint4 *>(buf + rb[t] + (p - MI) * (32 * KB * 16));
-  };
-  auto read_scales = [&](int slot, int win, int s) {
-    const uint8_t *p;
-    constexpr int step = S::WIDE ? 16 : 4;  // bytes between rows
-    if constexpr (S::WIDE)  // the lane's dword of the window; past the row's end: the last one
-      p = lds + S::WINDOWS + win * (S::ROWS * 16) + min(s * KB - min(s / 2 * 16, wlast) + 4 * hh, 12);
-    else
-      p = lds + slot * S::STAGE + S::ROWS * (KB * 16) + hh * (S::ROWS * 4);
-    p += (wm * (BM / S::WM) + li) * step;
+    for (int t = 0; t < KS; t++) {
+      const int c = ((t + 4 * hh) ^ tile_swizzle(li)) * 16;
+      ra[t] = (wm * (BM / S::WM) + li) * (KB * 16) + c;
+      rb[t] = (BM + wn * (BN / S::WN) + li) * (KB * 16) + c;
+    }
+    uint4 fa[2][MX], fb[2][NI];
+    uint32_t sa[2][MX], sb[2][NI];
+    auto read = [&](int slot, int t, int p) {  // fragment p (rows', then columns') of K step t of a stage
+      const uint8_t *buf = lds + slot * S::STAGE;
+      if (p < MX)
+        fa[t & 1][p] = *reinterpret_cast<const uint4 *>(buf + ra[t] + p * (32 * KB * 16));
+      else
+        fb[t & 1][p - MX] = *reinterpret_cast<const uint4 *>(buf + rb[t] + (p - MX) * (32 * KB * 16));
+    };
+    auto read_scales = [&](int slot, int win, int s) {
+      const uint8_t *p;
+      constexpr int step = S::WIDE ? 16 : 4;  // bytes between rows
+      if constexpr (S::WIDE)  // the lane's dword of the window; past the row's end: the last one
+        p = lds + S::WINDOWS + win * (S::ROWS * 16) + min(s * KB - min(s / 2 * 16, wlast) + 4 * hh, 12);
+      else
+        p = lds + slot * S::STAGE + S::ROWS * (KB * 16) + hh * (S::ROWS * 4);
+      p += (wm * (BM / S::WM) + li) * step;
 #pragma unroll
-    for (int i = 0; i < MI; i++) sa[1][i] = *reinterpret_cast<const uint32_t *>(p + i * 32 * step);
-    p += (BM + wn * (BN / S::WN) - wm * (BM / S::WM)) * step;
+      for (int i = 0; i < MX; i++) sa[1][i] = *reinterpret_cast<const uint32_t *>(p + i * 32 * step);
+      p += (BM + wn * (BN / S::WN) - wm * (BM / S::WM)) * step;
 #pragma unroll
-    for (int j = 0; j < NI; j++) sb[1][j] = *reinterpret_cast<const uint32_t *>(p + j * 32 * step);
-  };
-  auto take_scales = [&]() {
+      for (int j = 0; j < NI; j++) sb[1][j] = *reinterpret_cast<const uint32_t *>(p + j * 32 * step);
+    };
+    auto take_scales = [&]() {
 #pragma unroll
-    for (int i = 0; i < MI; i++) sa[0][i] = sa[1][i];
+      for (int i = 0; i < MX; i++) sa[0][i] = sa[1][i];
 #pragma unroll
-    for (int j = 0; j < NI; j++) sb[0][j] = sb[1][j];
-  };
-  auto mul = [&](int t, int i, int j) {
-    const uint4 x = fa[t & 1][i], y = fb[t & 1][j];
-    const uint32_t u = sa[0][i], v = sb[0][j];
-    acc[i][j] = t == 0 ? mx_mfma32<0>(x, u, y, v, acc[i][j]) : t == 1 ? mx_mfma32<1>(x, u, y, v, acc[i][j])
-              : t == 2 ? mx_mfma32<2>(x, u, y, v, acc[i][j]) : mx_mfma32<3>(x, u, y, v, acc[i][j]);
-  };
+      for (int j = 0; j < NI; j++) sb[0][j] = sb[1][j];
+    };
+    auto mul = [&](int t, int i, int j) {
+      const uint4 x = fa[t & 1][i], y = fb[t & 1][j];
+      const uint32_t u = sa[0][i], v = sb[0][j];
+      acc[i][j] = t == 0 ? mx_mfma32<0>(x, u, y, v, acc[i][j]) : t == 1 ? mx_mfma32<1>(x, u, y, v, acc[i][j])
+                : t == 2 ? mx_mfma32<2>(x, u, y, v, acc[i][j]) : mx_mfma32<3>(x, u, y, v, acc[i][j]);
+    };
 
-  // While a stage is multiplied the NBUF - 1 after it are on their way. Its last K step is in
-  // registers before its buffer is given up, and is multiplied while the loads of stage + NBUF
-  // and the first fragments of the next stage are under way. The products' part of the body
-  // has no branch: the compiler would move products across it, behind the wait.
+    // While a stage is multiplied the NBUF - 1 after it are on their way. Its last K step is in
+    // registers before its buffer is given up, and is multiplied while the loads of stage + NBUF
+    // and the first fragments of the next stage are under way. The products' part of the body
+    // has no branch: the compiler would move products across it, behind the wait.
 #pragma unroll
-  for (int s = 0; s < NBUF; s++) {
-    issue_start();
+    for (int s = 0; s < NBUF; s++) {
+      issue_start();
 #pragma unroll
-    for (int q = 0; q < ISSUES; q++) issue(q);
-    issue_end();
-  }
-  wait_loads<(NBUF - 1) * S::LOADS>();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  int cur = 0, cwin = 0;  // buffer slot and window of the stage that is multiplied
-  read_scales(0, 0, 0);
+      for (int q = 0; q < ISSUES; q++) issue(q);
+      issue_end();
+    }
+    wait_loads<(NBUF - 1) * LOADS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    int cur = 0, cwin = 0;  // buffer slot and window of the stage that is multiplied
+    read_scales(0, 0, 0);
 #pragma unroll
-  for (int p = 0; p < MI + NI; p++) read(0, 0, p);
-  take_scales();
-  for (int col = 0; col < cols; col++) {
+    for (int p = 0; p < MX + NI; p++) read(0, 0, p);
+    take_scales();
+    for (int col = 0; col < cols; col++) {
 #pragma unroll
-    for (int i = 0; i < MI; i++)
+      for (int i = 0; i < MX; i++)
 #pragma unroll
-      for (int j = 0; j < NI; j++) acc[i][j] = v16f{};
-    for (int s = 0; s < nst; s++) {
-      // products, fragment reads and loads take turns, in this order: the next step's fragments
-      // are read early in a step, and a burst of loads would leave the matrix cores without work
-      constexpr int MUL = MI * NI, RT = (MUL + 1) / 2, RP = (MI + NI + RT - 1) / RT;
+        for (int j = 0; j < NI; j++) acc[i][j] = v16f{};
+      for (int s = 0; s < nst; s++) {
+        // products, fragment reads and loads take turns, in this order: the next step's fragments
+        // are read early in a step, and a burst of loads would leave the matrix cores without work
+        constexpr int MUL = MX * NI, RT = (MUL + 1) / 2, RP = (MX + NI + RT - 1) / RT;
 #pragma unroll
-      for (int t = 0; t < KS - 1; t++)
+        for (int t = 0; t < KS - 1; t++)
+#pragma unroll
+          for (int q = 0; q < MUL; q++) {
+            mul(t, q / NI, q % NI);
+#pragma unroll
+            for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(cur, t + 1, p);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        const bool last = s == nst - 1;
+        const int next = cur == NBUF - 1 ? 0 : cur + 1, ns = last ? 0 : s + 1;
+        if ((s & 1) || last) cwin = cwin == S::NSB - 1 ? 0 : cwin + 1;
+        issue_start();
+        wait_loads<(NBUF - 2) * LOADS>();  // the next stage has arrived; this one is in registers
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        constexpr int PER = (ISSUES + MUL - 1) / MUL;
 #pragma unroll
         for (int q = 0; q < MUL; q++) {
-          mul(t, q / NI, q % NI);
-#pragma unroll
-          for (int p = q * RP; p < (q + 1) * RP && p < MI + NI; p++) read(cur, t + 1, p);
           __builtin_amdgcn_sched_barrier(0);
-        }
-      const bool last = s == nst - 1;
-      const int next = cur == NBUF - 1 ? 0 : cur + 1, ns = last ? 0 : s + 1;
-      if ((s & 1) || last) cwin = cwin == S::NSB - 1 ? 0 : cwin + 1;
-      issue_start();
-      wait_loads<(NBUF - 2) * S::LOADS>();  // the next stage has arrived; this one is in registers
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      constexpr int PER = (ISSUES + MUL - 1) / MUL;
+          mul(KS - 1, q / NI, q % NI);
+          if (q == 0) read_scales(next, cwin, ns);  // past the last stage: not used
 #pragma unroll
-      for (int q = 0; q < MUL; q++) {
+          for (int p = q * PER; p < (q + 1) * PER && p < ISSUES; p++) issue(p);
+#pragma unroll
+          for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(next, 0, p);
+        }
         __builtin_amdgcn_sched_barrier(0);
-        mul(KS - 1, q / NI, q % NI);
-        if (q == 0) read_scales(next, cwin, ns);  // past the last stage: not used
-#pragma unroll
-        for (int p = q * PER; p < (q + 1) * PER && p < ISSUES; p++) issue(p);
-#pragma unroll
-        for (int p = q * RP; p < (q + 1) * RP && p < MI + NI; p++) read(next, 0, p);
+        issue_end();
+        take_scales();
+        cur = next;
       }
-      __builtin_amdgcn_sched_barrier(0);
-      issue_end();
-      take_scales();
-      cur = next;
-    }
-    // results: lane column li of a 32 x 32 tile, rows 8 (r / 4) + 4 hh + r % 4
+      // results: lane column li of a 32 x 32 tile, rows 8 (r / 4) + 4 hh + r % 4. The stores have
+      // no branch (it would bring all results out of the accumulators at once): lanes without a
+      // row or column give an offset past the buffer's end, where a store is dropped.
+      const int c0 = (bx + col) * BF, nleft = a.N - c0;  // columns that exist
+      constexpr int NO = MODE == MX_GATEUP ? NI / 2 : NI;
+      int lo = li, ho = hh;
+      asm volatile("" : "+v"(lo), "+v"(ho));  // or the stores' offsets would all be kept over the column tiles
 #pragma unroll
-    for (int i = 0; i < MI; i++)
+      for (int i = 0; i < MX; i++)
 #pragma unroll
-      for (int r = 0; r < 16; r++) {
-        const int row = wm * (BM / S::WM) + i * 32 + 8 * (r / 4) + 4 * hh + (r & 3);
-        const int64_t o = out_row(row) * a.N + (bx + col) * BF;
-        const int nleft = row < n ? a.N - (bx + col) * BF : 0;  // columns that exist
-        if constexpr (MODE == MX_GATEUP) {
+        for (int q = 0; q < 4; q++) {
+          const int row = wm * (BM / S::WM) + i * 32 + 8 * q + 4 * ho;
 #pragma unroll
-          for (int j = 0; j < NI / 2; j++) {
-            const int c = wn * (BN / S::WN / 2) + j * 32 + li;
-            if (c < nleft) static_cast<T *>(a.out)[o + c] = (T)(silu(acc[i][j][r]) * acc[i][j + NI / 2][r]);
-          }
-        } else {
+          for (int j = 0; j < NO; j++) {
+            float v[4];
 #pragma unroll
-          for (int j = 0; j < NI; j++) {
-            const int c = wn * (BN / S::WN) + j * 32 + li;
-            if (c < nleft) static_cast<T *>(a.out)[o + c] = (T)acc[i][j][r];
+            for (int r = 0; r < 4; r++) {
+              v[r] = acc[i][j][4 * q + r];
+              if constexpr (MODE == MX_GATEUP) v[r] = silu(v[r]) * acc[i][j + NO][4 * q + r];
+            }
+            const int c = wn * (BF / S::WN) + j * 32 + lo;
+            if constexpr (VEC) {
+              // four columns of one row to a lane: stores of whole 64-byte pieces
+              auto w = quad_transpose<T>(v, lo & 3);
+              const int rr = row + (lo & 3), cc = c & ~3;
+              const uint32_t off = ((uint32_t)out_row(rr) * (uint32_t)a.N + c0 + cc) * sizeof(T);
+              store_out(w, out, rr < n && cc < nleft ? off : ~0u);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; r++) {
+                const uint32_t off = ((uint32_t)out_row(row + r) * (uint32_t)a.N + c0 + c) * sizeof(T);
+                store_out((T)v[r], out, row + r < n && c < nleft ? off : ~0u);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
-      }
+    }
+  };
+  // routed rows seldom fill a tile: the products of the 32-row tiles that hold none are left out
+  if constexpr (MODE == MX_LINEAR) {
+    run.template operator()<MI>();
+  } else {
+    static_assert(S::WM == 1 && MI == 4);
+    if (n <= 32)
+      run.template operator()<1>();
+    else if (n <= 64)
+      run.template operator()<2>();
+    else
+      run.template operator()<4>();
   }
 }
 
@@ -381,17 +463,32 @@ __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap
   if (tid == 0) *a.ntiles = min(total, cap);
 }
 
-template <MxMode MODE, typename T, typename S>
+// Column tiles of a dense workgroup: one workgroup runs on a CU at a time, and a strip's start
+// and end cost about a third of a tile.
+constexpr int MX_CUS = 256;
+static int dense_strip(int nx, int ny) {
+  int best = 1;
+  double cost = 1e300;
+  for (int s = 1; s <= 8 && s <= nx; s++) {
+    const int64_t groups = (int64_t)((nx + s - 1) / s) * ny;
+    const double c = (double)((groups + MX_CUS - 1) / MX_CUS) * (s + 0.33);
+    if (c < cost) cost = c, best = s;
+  }
+  return best;
+}
+
+template <MxMode MODE, typename T, typename S, bool VEC = true>
 static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static_assert(S::BYTES <= 160 * 1024, "LDS");
   constexpr int BF = MODE == MX_GATEUP ? S::BN / 2 : S::BN;
-  auto kernel = mx_tile_kernel<MODE, T, S>;
+  auto kernel = mx_tile_kernel<MODE, T, S, VEC>;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (attr != hipSuccess) return attr;
   const int nx = (a.N + BF - 1) / BF;
-  a.strip = STRIP;
-  const dim3 g = MODE == MX_LINEAR ? dim3((unsigned)(nx * ny)) : dim3((unsigned)((nx + a.strip - 1) / a.strip), (unsigned)ny);
+  a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny) : STRIP;
+  const unsigned gx = (unsigned)((nx + a.strip - 1) / a.strip);
+  const dim3 g = MODE == MX_LINEAR ? dim3(gx * (unsigned)ny) : dim3(gx, (unsigned)ny);
   hipLaunchKernelGGL(kernel, g, dim3(256), S::BYTES, s, a);
   return hipGetLastError();
 }
@@ -400,7 +497,7 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
 #define TD 256, 256, 2, 2, 2, 1
 #endif
 #ifndef TE
-#define TE 128, 256, 2, 2, 3, 1
+#define TE 128, 256, 1, 4, 3, 1
 #endif
 typedef TileShape<TD> TileDense;
 typedef TileShape<TE> TileExperts;
@@ -413,7 +510,10 @@ int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared) {
 
 template <typename T>
 static hipError_t launch_tile_t(MxMode mode, const MxArgs &a, hipStream_t s) {
-  if (mode == MX_LINEAR) return launch_tile<MX_LINEAR, T, TileDense>(a, (a.M + TileDense::BM - 1) / TileDense::BM, s);
+  if (mode == MX_LINEAR) {
+    const int ny = (a.M + TileDense::BM - 1) / TileDense::BM;
+    return a.N % 4 == 0 ? launch_tile<MX_LINEAR, T, TileDense>(a, ny, s) : launch_tile<MX_LINEAR, T, TileDense, false>(a, ny, s);
+  }
   const int cap = (int)mx_tile_cap(a.M, a.k, a.E, a.has_shared);
   hipLaunchKernelGGL(mx_plan_kernel, dim3(1), dim3(1024), 0, s, a, TileExperts::BM, cap);
   const hipError_t st = hipGetLastError();

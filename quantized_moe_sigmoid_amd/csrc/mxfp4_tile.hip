@@ -148,9 +148,16 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     first = by * BM;
     n = min(BM, a.M - first);
   } else {
-    bx = blockIdx.x * a.strip, by = blockIdx.y;
+    // Each XCD (id % 8) gets a run of row tiles, all column strips of one after another: the
+    // strips of a row tile share its activations in the XCD's L2, the row tiles of an expert
+    // its weights.
+    const int nt = *a.ntiles, ns = (nx + a.strip - 1) / a.strip, xcd = blockIdx.x & 7, total = nt * ns;
+    const int q = total >> 3, r = total & 7, local = blockIdx.x >> 3;
+    if (local >= q + (xcd < r)) return;
+    const int t = xcd * q + min(xcd, r) + local;
+    by = t / ns;
+    bx = (t - by * ns) * a.strip;
     cols = min(a.strip, nx - bx);
-    if (by >= *a.ntiles) return;
     const int4 c = a.tiles[by];
     e = c.x;
     first = c.y;
@@ -488,8 +495,8 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   const int nx = (a.N + BF - 1) / BF;
   a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny) : STRIP;
   const unsigned gx = (unsigned)((nx + a.strip - 1) / a.strip);
-  const dim3 g = MODE == MX_LINEAR ? dim3(gx * (unsigned)ny) : dim3(gx, (unsigned)ny);
-  hipLaunchKernelGGL(kernel, g, dim3(256), S::BYTES, s, a);
+  const unsigned groups = gx * (unsigned)ny;
+  hipLaunchKernelGGL(kernel, dim3(MODE == MX_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);
   return hipGetLastError();
 }
 

@@ -449,123 +449,134 @@ def make_router(n_experts, top_k, n_group=1, topk_group=1, score="sigmoid", grou
     return Router(n_experts, top_k, n_group, topk_group, group_top, _SCORES[score], int(bool(renorm)), scale)
 
 
+# Calls of a few microseconds: the checks below cost less than the launch they come before (one
+# pass over each tensor, the stream by its raw handle).
+_ELEM = {}
+
+
 def _elem(t, name) -> int:
     """coli_dtype of a tensor."""
-    import torch
-    d = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if not _ELEM:
+        import torch
+        _ELEM.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, "u8": torch.uint8, "i32": torch.int32,
+                      "f32": torch.float32, "stream": torch._C._cuda_getCurrentRawStream, "dev": torch._C._cuda_getDevice})
+    d = _ELEM.get(t.dtype)
     if d is None:
         raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
     return d
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != shape:
+def _arg(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of that type and shape (None: any) on GPU dev."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a CUDA (HIP) tensor on the call's device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _run(name, dev, stream, *args):
+    """Call entry point `name` with args and the stream, on GPU dev."""
+    if _ELEM["dev"]() != dev:
+        import torch
+        with torch.cuda.device(dev):
+            return _run(name, dev, stream, *args)
+    rc = getattr(lib(), name)(*args, _ELEM["stream"](dev) if stream is None else stream.cuda_stream)
+    if rc:
+        raise ColiError(rc, name)
 
 
 def route_logits(router: Router, logits, topk_idx, topk_w, bias=None, stream=None):
     """coli_moe_route_logits: logits [T][E] (fp32, bf16 or fp16) -> topk_idx int32, topk_w fp32 [T][k]."""
-    import torch
-    d = _elem(logits, "logits")
-    _dt(topk_idx, torch.int32, "topk_idx"), _dt(topk_w, torch.float32, "topk_w")
-    T = logits.shape[0]
-    _shape(logits, (T, router.n_experts), "logits")
-    _shape(topk_idx, (T, router.top_k), "topk_idx"), _shape(topk_w, (T, router.top_k), "topk_w")
-    if bias is not None:
-        _dt(bias, torch.float32, "bias"), _shape(bias, (router.n_experts,), "bias")
-    _check(lib().coli_moe_route_logits(C.byref(router), _ptr(logits), d, T, _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
-                                       _stream(stream, logits)), "coli_moe_route_logits")
+    d, dev = _elem(logits, "logits"), logits.get_device()
+    T, E, k = logits.shape[0], router.n_experts, router.top_k
+    f32 = _ELEM["f32"]
+    _run("coli_moe_route_logits", dev, stream, C.byref(router), _arg(logits, logits.dtype, (T, E), dev, "logits"), d, T,
+         None if bias is None else _arg(bias, f32, (E,), dev, "bias"),
+         _arg(topk_idx, _ELEM["i32"], (T, k), dev, "topk_idx"), _arg(topk_w, f32, (T, k), dev, "topk_w"))
 
 
-def _mx_shapes(rows, cols, codes, scales):
-    import torch
-    _dt(codes, torch.uint8, "codes"), _dt(scales, torch.uint8, "scales")
-    _shape(codes, (rows, cols // 2), "codes"), _shape(scales, (rows, cols // 32), "scales")
+def _packed(rows, cols, codes, scales, dev):
+    u8 = _ELEM["u8"]
+    return _arg(codes, u8, (rows, cols // 2), dev, "codes"), _arg(scales, u8, (rows, cols // 32), dev, "scales")
 
 
 def mxfp4_quantize(x, codes, scales, stream=None):
     """coli_moe_mxfp4_quantize: x [rows][cols] -> codes uint8 [rows][cols/2], scales uint8 [rows][cols/32]."""
     rows, cols = x.shape
-    d = _elem(x, "x")
-    _mx_shapes(rows, cols, codes, scales)
-    _check(lib().coli_moe_mxfp4_quantize(_ptr(x), d, rows, cols, _ptr(codes), _ptr(scales), _stream(stream, x)),
-           "coli_moe_mxfp4_quantize")
+    d, dev = _elem(x, "x"), x.get_device()
+    pc, ps = _packed(rows, cols, codes, scales, dev)
+    _run("coli_moe_mxfp4_quantize", dev, stream, _arg(x, x.dtype, None, dev, "x"), d, rows, cols, pc, ps)
 
 
 def mxfp4_dequantize(codes, scales, out, stream=None):
     """coli_moe_mxfp4_dequantize: codes, scales -> the values they stand for, out [rows][cols]."""
     rows, cols = out.shape
-    d = _elem(out, "out")
-    _mx_shapes(rows, cols, codes, scales)
-    _check(lib().coli_moe_mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), d, _stream(stream, out)),
-           "coli_moe_mxfp4_dequantize")
+    d, dev = _elem(out, "out"), out.get_device()
+    pc, ps = _packed(rows, cols, codes, scales, dev)
+    _run("coli_moe_mxfp4_dequantize", dev, stream, pc, ps, rows, cols, _arg(out, out.dtype, None, dev, "out"), d)
+
+
+def _workspace(name, *args):
+    import torch
+    n = int(getattr(lib(), name)(*args))
+    if n == 0:
+        raise ColiError(COLI_E_UNSUPPORTED, name)
+    return lambda device: torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def alloc_mxfp4_linear_workspace(M_max: int, N: int, K: int, device="cuda"):
-    import torch
-    n = int(lib().coli_moe_mxfp4_linear_workspace_bytes(M_max, N, K))
-    if n == 0:
-        raise ColiError(COLI_E_UNSUPPORTED, "coli_moe_mxfp4_linear_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _workspace("coli_moe_mxfp4_linear_workspace_bytes", M_max, N, K)(device)
 
 
 def mxfp4_linear(x, codes, scales, out, workspace, stream=None):
     """coli_moe_mxfp4_linear: out [M][N] = MXFP4(x [M][K]) W^T, W = codes [N][K/2] with scales [N][K/32]."""
     M, K = x.shape
     N = codes.shape[0]
+    dt, dev = x.dtype, x.get_device()
     d = _elem(x, "x")
-    _dt(out, x.dtype, "out"), _shape(out, (M, N), "out")
-    _mx_shapes(N, K, codes, scales)
-    _check(lib().coli_moe_mxfp4_linear(_ptr(x), d, _ptr(codes), _ptr(scales), M, N, K, _ptr(out), _ptr(workspace),
-                                       workspace.numel(), _stream(stream, x)), "coli_moe_mxfp4_linear")
+    pc, ps = _packed(N, K, codes, scales, dev)
+    _run("coli_moe_mxfp4_linear", dev, stream, _arg(x, dt, None, dev, "x"), d, pc, ps, M, N, K,
+         _arg(out, dt, (M, N), dev, "out"), _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
 
 
 def alloc_mxfp4_experts_workspace(cfg: Cfg, T_max: int, device="cuda"):
-    import torch
-    n = int(lib().coli_moe_mxfp4_experts_workspace_bytes(C.byref(cfg), T_max))
-    if n == 0:
-        raise ColiError(COLI_E_UNSUPPORTED, "coli_moe_mxfp4_experts_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _workspace("coli_moe_mxfp4_experts_workspace_bytes", C.byref(cfg), T_max)(device)
 
 
-def _mx_experts(cfg, w, T, off, perm, active, n_active):
-    import torch
-    E, S = cfg.n_experts, cfg.has_shared
-    n = 3 * cfg.hidden * cfg.ffn
-    _dt(w.experts, torch.uint8, "experts"), _dt(w.scales, torch.uint8, "scales")
-    if w.experts.numel() != (E + S) * (n // 2) or w.scales.numel() != (E + S) * (n // 32):
+def _mx_weights(cfg, w, dev):
+    u8, n = _ELEM["u8"], (cfg.n_experts + cfg.has_shared) * 3 * cfg.hidden * cfg.ffn
+    if w.experts.numel() != n // 2 or w.scales.numel() != n // 32:
         raise ValueError("weights: sizes do not match the configuration")
-    for name, t, size in (("off", off, E + 1), ("perm", perm, T * cfg.top_k), ("active", active, E),
-                          ("n_active", n_active, 1)):
-        _dt(t, torch.int32, name)
-        if t.numel() != size:
-            raise ValueError(f"{name}: expected {size} elements, got {t.numel()}")
+    return C.byref(_Weights(_arg(w.experts, u8, None, dev, "experts"), _arg(w.scales, u8, None, dev, "scales"), None, None))
+
+
+def _grouping(cfg, T, off, perm, active, n_active, dev):
+    i32, E = _ELEM["i32"], cfg.n_experts
+    return (_arg(off, i32, (E + 1,), dev, "off"), _arg(perm, i32, (T * cfg.top_k,), dev, "perm"),
+            _arg(active, i32, (E,), dev, "active"), _arg(n_active, i32, (1,), dev, "n_active"))
 
 
 def mxfp4_gate_up(cfg: Cfg, w: Weights, x, off, perm, active, n_active, h, workspace, stream=None):
     """coli_moe_mxfp4_gate_up: h [T k + T shared][F] = silu(gate) * up of every pair of the route."""
-    T = x.shape[0]
+    T, dt, dev = x.shape[0], x.dtype, x.get_device()
     d = _elem(x, "x")
-    _shape(x, (T, cfg.hidden), "x"), _dt(h, x.dtype, "h")
-    _shape(h, (T * (cfg.top_k + cfg.has_shared), cfg.ffn), "h")
-    _mx_experts(cfg, w, T, off, perm, active, n_active)
-    wc = w.c()
-    _check(lib().coli_moe_mxfp4_gate_up(C.byref(cfg), C.byref(wc), _ptr(x), d, T, _ptr(off), _ptr(perm), _ptr(active),
-                                        _ptr(n_active), _ptr(h), _ptr(workspace), workspace.numel(),
-                                        _stream(stream, x)), "coli_moe_mxfp4_gate_up")
+    _run("coli_moe_mxfp4_gate_up", dev, stream, C.byref(cfg), _mx_weights(cfg, w, dev),
+         _arg(x, dt, (T, cfg.hidden), dev, "x"), d, T, *_grouping(cfg, T, off, perm, active, n_active, dev),
+         _arg(h, dt, (T * (cfg.top_k + cfg.has_shared), cfg.ffn), dev, "h"),
+         _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
 
 
 def mxfp4_down(cfg: Cfg, w: Weights, h, topk_idx, topk_w, off, perm, active, n_active, out, workspace, stream=None):
     """coli_moe_mxfp4_down: out [T][H] = the pairs' down rows, weighted and summed, + the shared expert's."""
-    import torch
-    T = topk_idx.shape[0]
+    T, dt, dev, k = topk_idx.shape[0], h.dtype, h.get_device(), cfg.top_k
     d = _elem(h, "h")
-    _shape(h, (T * (cfg.top_k + cfg.has_shared), cfg.ffn), "h"), _dt(out, h.dtype, "out")
-    _shape(out, (T, cfg.hidden), "out")
-    _dt(topk_idx, torch.int32, "topk_idx"), _dt(topk_w, torch.float32, "topk_w")
-    _shape(topk_idx, (T, cfg.top_k), "topk_idx"), _shape(topk_w, (T, cfg.top_k), "topk_w")
-    _mx_experts(cfg, w, T, off, perm, active, n_active)
-    wc = w.c()
-    _check(lib().coli_moe_mxfp4_down(C.byref(cfg), C.byref(wc), _ptr(h), d, T, _ptr(topk_idx), _ptr(topk_w), _ptr(off),
-                                     _ptr(perm), _ptr(active), _ptr(n_active), _ptr(out), _ptr(workspace),
-                                     workspace.numel(), _stream(stream, h)), "coli_moe_mxfp4_down")
+    _run("coli_moe_mxfp4_down", dev, stream, C.byref(cfg), _mx_weights(cfg, w, dev),
+         _arg(h, dt, (T * (k + cfg.has_shared), cfg.ffn), dev, "h"), d, T,
+         _arg(topk_idx, _ELEM["i32"], (T, k), dev, "topk_idx"), _arg(topk_w, _ELEM["f32"], (T, k), dev, "topk_w"),
+         *_grouping(cfg, T, off, perm, active, n_active, dev), _arg(out, dt, (T, cfg.hidden), dev, "out"),
+         _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())

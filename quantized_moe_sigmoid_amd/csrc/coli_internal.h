@@ -237,6 +237,7 @@ struct MxArgs {
   int64_t wc_stride, ws_stride;   // bytes per expert
   int32_t ws_pitch;               // bytes of scales per weight row
   int32_t N, K;                   // output columns (weight rows of a matrix), inputs
+  const void *x;                  // activations that the kernel quantises itself (null: those below)
   const uint8_t *ac, *as;         // quantised activations, rows of mx_padded(K)
   int32_t M;                      // rows (linear); tokens (experts)
   int32_t E, k, has_shared;       // experts only, as is the grouping below
@@ -254,7 +255,11 @@ hipError_t launch_mx_quantize_rows(const void *x, int dtype, int64_t rows, int K
                                    hipStream_t s);
 // rows of nb scale bytes copied to a pitch of mx_padded(32 nb) / 32, the rest set to 1
 hipError_t launch_mx_pad_scales(const uint8_t *scales, int rows, int K, uint8_t *out, hipStream_t s);
-hipError_t launch_mx_product(MxMode mode, int dtype, const MxArgs &a, hipStream_t s);
+hipError_t launch_mx_gemv(MxMode mode, int dtype, const MxArgs &a, hipStream_t s);
+bool mx_gemv_from_x(const MxArgs &a);  // launch_mx_gemv with x set takes these sizes
+bool mx_down_fused(const MxArgs &a);   // launch_mx_down takes these sizes, with x set:
+bool mx_down_from_x(const MxArgs &a);
+hipError_t launch_mx_down(const MxArgs &a, const int32_t *idx, const float *w, void *out, int dtype, hipStream_t s);
 hipError_t launch_mx_tile(MxMode mode, int dtype, const MxArgs &a, hipStream_t s);
 int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared);  // most row tiles of a route
 hipError_t launch_mx_combine(const float *y, const int32_t *idx, const float *w, int T, int k, int E, int H,

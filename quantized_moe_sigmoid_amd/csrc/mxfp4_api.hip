@@ -76,7 +76,7 @@ static MxArgs expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
 
 static hipError_t launch_experts(MxMode mode, int dtype, MxArgs &a, uint8_t *ws, const MxWs &L, hipStream_t s) {
   a.ws_pitch = a.K / 32;
-  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P) return launch_mx_product(mode, dtype, a, s);
+  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P) return launch_mx_gemv(mode, dtype, a, s);
   a.tiles = reinterpret_cast<int4 *>(ws + L.tiles);
   a.ntiles = reinterpret_cast<int32_t *>(ws + L.ntiles);
   return launch_mx_tile(mode, dtype, a, s);
@@ -160,7 +160,6 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
   if (!mx_aligned(workspace, 256)) return COLI_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if ((st = mx_dev(launch_mx_quantize_rows(x, dtype, M, K, ws + L.ac, ws + L.as, s)))) return st;
   MxArgs a{};
   a.wc = codes;
   a.ws = scales;
@@ -171,7 +170,11 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
   a.M = M;
   a.out = y;
   a.ws_pitch = K / 32;
-  if (M <= MX_ROWS_TILE) return mx_dev(launch_mx_product(MX_LINEAR, dtype, a, s));
+  if (mx_gemv_from_x(a))
+    a.x = x;
+  else if ((st = mx_dev(launch_mx_quantize_rows(x, dtype, M, K, ws + L.ac, ws + L.as, s))))
+    return st;
+  if (M <= MX_ROWS_TILE) return mx_dev(launch_mx_gemv(MX_LINEAR, dtype, a, s));
   if (K % 128 || K < 512 || !mx_aligned(scales, 4)) {  // the tiled kernel loads 16 scales at a dword's address
     if ((st = mx_dev(launch_mx_pad_scales(scales, N, K, ws + L.y, s)))) return st;
     a.ws = ws + L.y;
@@ -202,10 +205,13 @@ int coli_moe_mxfp4_gate_up(const coli_moe_cfg *cfg, const coli_moe_weights *w, c
   if (!mx_aligned(workspace, 256)) return COLI_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if ((st = mx_dev(launch_mx_quantize_rows(x, dtype, T, cfg->hidden, ws + L.ac, ws + L.as, s)))) return st;
   MxArgs a = expert_args(*cfg, *w, T, expert_off, pair_perm, active, n_active);
   a.N = cfg->ffn;
   a.K = cfg->hidden;
+  if (mx_gemv_from_x(a))
+    a.x = x;
+  else if ((st = mx_dev(launch_mx_quantize_rows(x, dtype, T, cfg->hidden, ws + L.ac, ws + L.as, s))))
+    return st;
   a.ac = ws + L.ac;
   a.as = ws + L.as;
   a.out = h;
@@ -228,7 +234,6 @@ int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, cons
   if (!mx_aligned(workspace, 256)) return COLI_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  if ((st = mx_dev(launch_mx_quantize_rows(h, dtype, mx_rows(*cfg, T), cfg->ffn, ws + L.ac, ws + L.as, s)))) return st;
   MxArgs a = expert_args(*cfg, *w, T, expert_off, pair_perm, active, n_active);
   a.wc += (int64_t)cfg->ffn * cfg->hidden;  // gate and up rows: 2 F H / 2 bytes
   a.ws += (int64_t)cfg->ffn * cfg->hidden / 16;
@@ -237,6 +242,12 @@ int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, cons
   a.ac = ws + L.ac;
   a.as = ws + L.as;
   a.out = ws + L.y;
+  const bool fused = mx_down_fused(a);
+  if (fused && mx_down_from_x(a))
+    a.x = h;
+  else if ((st = mx_dev(launch_mx_quantize_rows(h, dtype, mx_rows(*cfg, T), cfg->ffn, ws + L.ac, ws + L.as, s))))
+    return st;
+  if (fused) return mx_dev(launch_mx_down(a, topk_idx, topk_w, out, dtype, s));
   if ((st = mx_dev(launch_experts(MX_DOWN, dtype, a, ws, L, s)))) return st;
   return mx_dev(launch_mx_combine(reinterpret_cast<float *>(ws + L.y), topk_idx, topk_w, T, cfg->top_k,
                                   cfg->n_experts, cfg->hidden, cfg->has_shared, out, dtype, s));

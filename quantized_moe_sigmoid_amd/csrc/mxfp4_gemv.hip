@@ -1,0 +1,439 @@
+// mxfp4_gemv.hip — MXFP4 x MXFP4 products of few rows, bound by the weights' way from HBM: dense
+// rows, the experts' gate/up rows with SiLU*up and their down rows over a route (batch-union:
+// colibri-strix README, "What's implemented"), on the scaled 16x16x128 matrix instruction.
+//
+// mx_gemv_kernel: a workgroup (4 wavefronts) owns 16 weight rows (of each matrix) and chunks of
+// 16 NT rows of activations. The wavefronts take the K groups (16 blocks, 512 inputs: 256
+// contiguous bytes of a row) in turn, two groups of weights under way at a time straight into
+// the operand registers; their sums meet in LDS, added in wavefront order. One row of
+// activations (x in ACT_X) is quantised by every workgroup itself while its first weights are
+// under way, which saves a launch.
+//
+// mx_down_kernel: the down product of up to 16 tokens with its weighted combine. A workgroup (8
+// wavefronts) owns 16 output rows of every token and goes through all experts of the route, a
+// token to a column of the matrix instruction; the (expert, K group) units go to the wavefronts
+// in turn. No rows per pair are written, no second kernel sums them.
+#include "mxfp4_impl.h"
+
+namespace coli {
+
+// 16 blocks of a weight row, as a lane of the matrix instruction takes them: in step s the
+// block 4 s + l / 16; u[s] holds its scale in byte 0
+struct Group {
+  uint4 c[4];
+  uint32_t u[4];
+};
+
+// Group g of a row of nb blocks; AL16: nb is a multiple of 16 and the scales are 16-byte aligned
+template <bool AL16>
+__device__ __forceinline__ void load_group(const uint8_t *codes, const uint8_t *scales, int nb, int g, int lq, Group &o) {
+  if constexpr (AL16) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(scales + g * 16);
+    o.u[0] = u.x, o.u[1] = u.y, o.u[2] = u.z, o.u[3] = u.w;  // shifted at the product
+  }
+#pragma unroll
+  for (int s = 0; s < 4; s++) {
+    const int b = g * 16 + 4 * s + lq;
+    if constexpr (AL16) {
+      o.c[s] = *reinterpret_cast<const uint4 *>(codes + b * 16);
+    } else {
+      const int bb = min(b, nb - 1);  // past the row: the last block; it meets activations of zero
+      o.c[s] = *reinterpret_cast<const uint4 *>(codes + bb * 16);
+      o.u[s] = scales[bb];
+    }
+  }
+}
+
+template <bool AL16>
+__device__ __forceinline__ uint32_t group_scale(const Group &g, int s, int lq) {
+  return AL16 ? g.u[s] >> (8 * lq) : g.u[s];
+}
+
+// One row x of nb blocks -> codes and scales in LDS (blocks nb .. nbp: zeros), by 256 threads.
+// The values of a thread's first two half-blocks come in v (load_x), loaded ahead.
+constexpr int XH = 2;
+template <typename T>
+__device__ __forceinline__ void load_x(const T *x, int nb, int tid, float (&v)[XH][2][8]) {
+#pragma unroll
+  for (int i = 0; i < XH; i++) {
+    const int h = min(tid + 256 * i, 2 * nb - 1), blk = h >> 1, q = h & 1;
+    load8(x + blk * 32 + 8 * q, v[i][0]);
+    load8(x + blk * 32 + 16 + 8 * q, v[i][1]);
+  }
+}
+
+__device__ __forceinline__ void put_half(uint8_t *lc, uint8_t *ls, int h, const float (&a)[8], const float (&b)[8]) {
+  uint32_t u;
+  const uint2 w = mx_quant_half(a, b, u);
+  *reinterpret_cast<uint2 *>(lc + h * 8) = w;
+  if (!(h & 1)) ls[h >> 1] = (uint8_t)u;
+}
+
+template <typename T>
+__device__ __forceinline__ void quantise_x(const T *x, int nb, int nbp, int tid, const float (&v)[XH][2][8], uint8_t *lc,
+                                           uint8_t *ls) {
+#pragma unroll
+  for (int i = 0; i < XH; i++) {
+    const int h = tid + 256 * i;
+    if (h < 2 * nb) put_half(lc, ls, h, v[i][0], v[i][1]);  // both lanes of a block or neither
+  }
+  for (int h = tid + 256 * XH; h < 2 * nb; h += 256) {
+    float a[8], b[8];
+    load8(x + (h >> 1) * 32 + 8 * (h & 1), a);
+    load8(x + (h >> 1) * 32 + 16 + 8 * (h & 1), b);
+    put_half(lc, ls, h, a, b);
+  }
+  for (int h = 2 * nb + tid; h < 2 * nbp; h += 256) {
+    *reinterpret_cast<uint2 *>(lc + h * 8) = make_uint2(0, 0);
+    if (!(h & 1)) ls[h >> 1] = 127;
+  }
+}
+
+enum MxAct { ACT_WS, ACT_X };  // activations: quantised in the workspace; one row of x
+
+template <MxMode MODE, typename T, int NT, MxAct ACT, bool AL16>
+__global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
+  constexpr int NMAT = MODE == MX_GATEUP ? 2 : 1;
+  constexpr int D = NT == 4 ? 1 : 2;  // groups under way: what the registers hold
+  static_assert(ACT == ACT_WS || (NT == 1 && MODE != MX_DOWN));
+  extern __shared__ __align__(16) uint8_t lds[];  // ACT_X: the quantised row
+  __shared__ float red[4][NMAT][NT][16][17];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int li = lane & 15, lq = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int nb = a.K / 32, nbp = mx_padded(a.K) / 32;
+  const int ngw = (nbp / 16 - wv + 3) / 4;  // groups of this wavefront: wv, wv + 4, ..
+  // the rows of activations: first .. first + n - 1 of perm (routed) or of the tokens
+  int e = 0, first = 0, n = a.M;
+  bool routed = false;
+  if constexpr (MODE == MX_LINEAR) {
+    first = blockIdx.y * (16 * NT);
+    n = min(16 * NT, a.M - first);
+  } else {
+    const int u = (int)blockIdx.y - a.has_shared;
+    if (u < 0) {
+      e = a.E;
+    } else {
+      const int na = max(0, min(*a.nact, a.E));
+      if (u >= na) return;
+      e = a.active[u];
+      first = a.off[e];
+      n = a.off[e + 1] - first;
+      routed = true;
+    }
+  }
+  const int64_t P = (int64_t)a.M * a.k;
+  float xv[XH][2][8];
+  const T *x = static_cast<const T *>(a.x);
+  if constexpr (ACT == ACT_X) {
+    load_x(x, nb, tid, xv);
+  }
+  const uint8_t *wc[NMAT], *ws[NMAT];
+#pragma unroll
+  for (int m = 0; m < NMAT; m++) {
+    const int64_t row = (int64_t)m * a.N + min(n0 + li, a.N - 1);
+    wc[m] = a.wc + (int64_t)e * a.wc_stride + row * nb * 16;
+    ws[m] = a.ws + (int64_t)e * a.ws_stride + row * nb;
+  }
+  Group w[D][NMAT], act[D][NT];
+  for (int c = 0; c < n; c += 16 * NT) {
+    const uint8_t *ac[NT], *as[NT];
+    if constexpr (ACT == ACT_WS) {
+#pragma unroll
+      for (int q = 0; q < NT; q++) {
+        const int ci = first + min(c + 16 * q + li, n - 1);
+        int64_t arow = ci;
+        if constexpr (MODE != MX_LINEAR) {
+          const int64_t pair = routed ? a.perm[ci] : P + ci;
+          arow = MODE == MX_DOWN ? pair : (routed ? pair / a.k : ci);
+        }
+        ac[q] = a.ac + arow * nbp * 16;
+        as[q] = a.as + arow * nbp;
+      }
+    }
+    // group i of this wavefront: weights and (in the workspace) activations together, since
+    // loads arrive in order
+    auto load_act = [&](int d, int i) {
+#pragma unroll
+      for (int q = 0; q < NT; q++) load_group<true>(ac[q], as[q], nbp, wv + 4 * i, lq, act[d][q]);
+    };
+    auto load = [&](int d, int i) {
+#pragma unroll
+      for (int m = 0; m < NMAT; m++) load_group<AL16>(wc[m], ws[m], nb, wv + 4 * i, lq, w[d][m]);
+      if constexpr (ACT == ACT_WS) load_act(d, i);
+    };
+#pragma unroll
+    for (int d = 0; d < D; d++)
+      if (d < ngw) load(d, d);
+    if constexpr (ACT == ACT_X) {
+      quantise_x(x, nb, nbp, tid, xv, lds, lds + nbp * 16);
+      __syncthreads();
+      ac[0] = lds;
+      as[0] = lds + nbp * 16;
+    }
+    v4f acc[NT][NMAT] = {};
+    for (int i0 = 0; i0 < ngw; i0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; d++) {
+        if (i0 + d < ngw) {
+          if constexpr (ACT == ACT_X) load_act(d, i0 + d);
+#pragma unroll
+          for (int s = 0; s < 4; s++)
+#pragma unroll
+            for (int q = 0; q < NT; q++)
+#pragma unroll
+              for (int m = 0; m < NMAT; m++)
+                acc[q][m] = mx_mfma16(act[d][q].c[s], group_scale<true>(act[d][q], s, lq), w[d][m].c[s],
+                                      group_scale<AL16>(w[d][m], s, lq), acc[q][m]);
+          if (i0 + d + D < ngw) load(d, i0 + d + D);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NT; q++)
+#pragma unroll
+      for (int m = 0; m < NMAT; m++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) red[wv][m][q][4 * lq + r][li] = acc[q][m][r];
+    __syncthreads();
+    const int tr = tid >> 4, tc = tid & 15;
+#pragma unroll
+    for (int q = 0; q < NT; q++) {
+      float v[NMAT];
+#pragma unroll
+      for (int m = 0; m < NMAT; m++)
+        v[m] = ((red[0][m][q][tr][tc] + red[1][m][q][tr][tc]) + red[2][m][q][tr][tc]) + red[3][m][q][tr][tc];
+      const int row = c + 16 * q + tr;
+      if (row < n && n0 + tc < a.N) {
+        const int ci = first + row;
+        const int64_t orow = MODE == MX_LINEAR ? ci : (routed ? (int64_t)a.perm[ci] : P + ci);
+        const int64_t o = orow * a.N + n0 + tc;
+        if constexpr (MODE == MX_GATEUP)
+          static_cast<T *>(a.out)[o] = (T)(silu(v[0]) * v[1]);
+        else if constexpr (MODE == MX_DOWN)
+          static_cast<float *>(a.out)[o] = v[0];
+        else
+          static_cast<T *>(a.out)[o] = (T)v[0];
+      }
+    }
+    if (c + 16 * NT < n) __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ down with its combine
+constexpr int DN_TOK = 16, DN_K = 16, DN_WAVES = 8, DN_DEPTH = 2;
+
+template <typename T, MxAct ACT, bool AL16>
+__global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, const int32_t *__restrict__ idx,
+                                                               const float *__restrict__ w, T *__restrict__ out) {
+  // slots[e * 16 + t]: the slots of token t that hold expert e, a bit each; the experts of the
+  // route; ACT_X: the quantised rows
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ float red[DN_WAVES][16][17];
+  uint16_t *slots = reinterpret_cast<uint16_t *>(lds);
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, lq = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, ng = nbp / 16;
+  const int T_ = a.M, k = a.k, E = a.E, P = T_ * k;
+  for (int i = tid; i < E * DN_TOK / 2; i += 64 * DN_WAVES) reinterpret_cast<uint32_t *>(slots)[i] = 0;
+  int *active = reinterpret_cast<int *>(lds + E * DN_TOK * 2);
+  const int na = max(0, min(*a.nact, E)), units = (na + a.has_shared) * ng;
+  for (int i = tid; i < na; i += 64 * DN_WAVES) active[i] = a.active[i];
+  uint8_t *lc = lds + (E * (DN_TOK * 2 + 4) + 15) / 16 * 16, *ls = lc;
+  if constexpr (ACT == ACT_X) {
+    ls = lc + (P + a.has_shared) * nbp * 16;
+    const T *x = static_cast<const T *>(a.x);
+    for (int h = tid; h < (P + a.has_shared) * nbp * 2; h += 64 * DN_WAVES) {
+      const int row = h / (2 * nbp), hb = h - row * 2 * nbp, blk = hb >> 1, q = hb & 1;
+      float va[8], vb[8];
+      uint2 c = make_uint2(0, 0);
+      uint32_t u = 127;
+      if (blk < nb) {
+        load8(x + ((int64_t)row * nb + blk) * 32 + 8 * q, va);
+        load8(x + ((int64_t)row * nb + blk) * 32 + 16 + 8 * q, vb);
+        c = mx_quant_half(va, vb, u);
+      }
+      *reinterpret_cast<uint2 *>(lc + h * 8) = c;
+      if (q == 0) ls[h >> 1] = (uint8_t)u;
+    }
+  }
+  __syncthreads();
+  if (tid < T_)
+    for (int j = 0; j < k; j++) {
+      const int e = idx[tid * k + j];
+      if (e >= 0 && e < E) slots[e * DN_TOK + tid] |= (uint16_t)(1u << j);
+    }
+  __syncthreads();
+  const int wrow = n0 + li;  // N is a multiple of 128
+  const uint8_t *ac = ACT == ACT_X ? lc : a.ac, *as = ACT == ACT_X ? ls : a.as;
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  Group wg[DN_DEPTH], act[DN_DEPTH];
+  uint32_t held[DN_DEPTH];  // slots of this lane's token that hold a unit's expert
+  float wt[DN_DEPTH];       // weight of the first
+  // A token's lanes take the row of slot j of unit (e, g), or any row where there is none.
+  auto load_act = [&](int d, int e, int g, uint32_t mine) {
+    const int j = mine ? __builtin_ctz(mine) : 0, p = e < E ? li * k + j : P + li;
+    const int row = mine ? p : (e < E ? 0 : P);
+    load_group<true>(ac + (int64_t)row * nbp * 16, as + (int64_t)row * nbp, nbp, g, lq, act[d]);
+    wt[d] = !mine ? 0.0f : e < E ? w[p] : 1.0f;
+  };
+  // weights and activations of a unit together, since loads arrive in order
+  auto load = [&](int d, int u) {
+    const int s = u / ng, g = u - s * ng;
+    const int e = s < na ? __builtin_amdgcn_readfirstlane(active[s]) : E;
+    const uint8_t *wc = a.wc + (int64_t)e * a.wc_stride + (int64_t)wrow * nb * 16;
+    const uint8_t *ws = a.ws + (int64_t)e * a.ws_stride + (int64_t)wrow * nb;
+    load_group<AL16>(wc, ws, nb, g, lq, wg[d]);
+    held[d] = li < T_ ? (e < E ? slots[e * DN_TOK + li] : 1u) : 0u;
+    load_act(d, e, g, held[d]);
+  };
+#pragma unroll
+  for (int d = 0; d < DN_DEPTH; d++)
+    if (wv + DN_WAVES * d < units) load(d, wv + DN_WAVES * d);
+  for (int u0 = wv; u0 < units; u0 += DN_WAVES * DN_DEPTH) {
+#pragma unroll
+    for (int d = 0; d < DN_DEPTH; d++) {
+      const int u = u0 + DN_WAVES * d;
+      if (u < units) {
+        uint32_t mine = held[d];
+        while (true) {
+          v4f dsum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < 4; s++)  // rows of the result: weight rows; columns: tokens
+            dsum = mx_mfma16(wg[d].c[s], group_scale<AL16>(wg[d], s, lq), act[d].c[s], group_scale<true>(act[d], s, lq), dsum);
+#pragma unroll
+          for (int r = 0; r < 4; r++) acc[r] = mine ? __builtin_fmaf(wt[d], dsum[r], acc[r]) : acc[r];
+          // a token holds an expert in one slot; a route that repeats one takes another round
+          mine &= mine - 1;
+          if (__builtin_expect(__ballot(mine != 0) == 0, 1)) break;
+          const int s = u / ng;
+          load_act(d, active[s], u - s * ng, mine);  // (the shared expert is held once)
+        }
+        if (u + DN_WAVES * DN_DEPTH < units) load(d, u + DN_WAVES * DN_DEPTH);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; r++) red[wv][li][4 * lq + r] = acc[r];
+  __syncthreads();
+  const int t = tid >> 4, r = tid & 15;
+  if (t < T_) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < DN_WAVES; i++) s += red[i][t][r];
+    out[(int64_t)t * a.N + n0 + r] = (T)s;
+  }
+}
+
+// LDS of mx_down_kernel, and of its rows when it quantises them itself
+static size_t down_lds(const MxArgs &a, bool x) {
+  const size_t nbp = mx_padded(a.K) / 32;
+  return ((size_t)a.E * (DN_TOK * 2 + 4) + 15) / 16 * 16 + (x ? ((size_t)a.M * a.k + (size_t)a.M * a.has_shared) * nbp * 17 : 0);
+}
+
+bool mx_down_fused(const MxArgs &a) { return a.M <= DN_TOK && a.k <= DN_K; }
+bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && down_lds(a, true) <= 56 * 1024; }
+// One row quantised by every workgroup
+bool mx_gemv_from_x(const MxArgs &a) { return a.M == 1 && mx_padded(a.K) / 32 * 17 <= 48 * 1024; }
+
+static bool scales_al16(const MxArgs &a) {
+  return (a.K / 32) % 16 == 0 && (uintptr_t)a.ws % 16 == 0 && a.ws_stride % 16 == 0;
+}
+
+template <MxMode MODE, typename T, int NT, MxAct ACT>
+static hipError_t launch_gemv_al(const MxArgs &a, int ny, size_t lds, hipStream_t s) {
+  const dim3 g((unsigned)((a.N + 15) / 16), (unsigned)ny), b(256);
+  const bool al16 = scales_al16(a);
+  if (al16)
+    hipLaunchKernelGGL((mx_gemv_kernel<MODE, T, NT, ACT, true>), g, b, lds, s, a);
+  else
+    hipLaunchKernelGGL((mx_gemv_kernel<MODE, T, NT, ACT, false>), g, b, lds, s, a);
+  return hipGetLastError();
+}
+
+template <MxMode MODE, typename T>
+static hipError_t launch_gemv_t(const MxArgs &a, hipStream_t s) {
+  const int64_t P = (int64_t)a.M * a.k;
+  const size_t xlds = (size_t)(mx_padded(a.K) / 32) * 17;
+  if constexpr (MODE == MX_LINEAR) {
+    if (a.x) return launch_gemv_al<MODE, T, 1, ACT_X>(a, 1, xlds, s);
+    if (a.M <= 16) return launch_gemv_al<MODE, T, 1, ACT_WS>(a, 1, 0, s);
+    if (a.M <= 32) return launch_gemv_al<MODE, T, 2, ACT_WS>(a, 1, 0, s);
+    return launch_gemv_al<MODE, T, 4, ACT_WS>(a, (a.M + 63) / 64, 0, s);
+  } else {
+    const int ny = a.has_shared + (int)(P < a.E ? P : a.E);
+    if constexpr (MODE == MX_GATEUP)
+      if (a.x) return launch_gemv_al<MODE, T, 1, ACT_X>(a, ny, xlds, s);
+    return launch_gemv_al<MODE, T, 1, ACT_WS>(a, ny, 0, s);
+  }
+}
+
+hipError_t launch_mx_gemv(MxMode mode, int dtype, const MxArgs &a, hipStream_t s) {
+  if (mode == MX_DOWN) return launch_gemv_t<MX_DOWN, float>(a, s);
+  if (mode == MX_LINEAR)
+    return dtype == COLI_F32 ? launch_gemv_t<MX_LINEAR, float>(a, s)
+         : dtype == COLI_BF16 ? launch_gemv_t<MX_LINEAR, bf16_t>(a, s) : launch_gemv_t<MX_LINEAR, f16_t>(a, s);
+  return dtype == COLI_F32 ? launch_gemv_t<MX_GATEUP, float>(a, s)
+       : dtype == COLI_BF16 ? launch_gemv_t<MX_GATEUP, bf16_t>(a, s) : launch_gemv_t<MX_GATEUP, f16_t>(a, s);
+}
+
+template <typename T>
+static hipError_t launch_down_t(const MxArgs &a, const int32_t *idx, const float *w, void *out, hipStream_t s) {
+  const dim3 g((unsigned)(a.N / 16)), b(64 * DN_WAVES);
+  const size_t lds = down_lds(a, a.x != nullptr);
+  const bool al16 = scales_al16(a);
+  if (a.x && al16)
+    hipLaunchKernelGGL((mx_down_kernel<T, ACT_X, true>), g, b, lds, s, a, idx, w, (T *)out);
+  else if (a.x)
+    hipLaunchKernelGGL((mx_down_kernel<T, ACT_X, false>), g, b, lds, s, a, idx, w, (T *)out);
+  else if (al16)
+    hipLaunchKernelGGL((mx_down_kernel<T, ACT_WS, true>), g, b, lds, s, a, idx, w, (T *)out);
+  else
+    hipLaunchKernelGGL((mx_down_kernel<T, ACT_WS, false>), g, b, lds, s, a, idx, w, (T *)out);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_down(const MxArgs &a, const int32_t *idx, const float *w, void *out, int dtype, hipStream_t s) {
+  if (dtype == COLI_F32) return launch_down_t<float>(a, idx, w, out, s);
+  if (dtype == COLI_BF16) return launch_down_t<bf16_t>(a, idx, w, out, s);
+  return launch_down_t<f16_t>(a, idx, w, out, s);
+}
+
+// out_t = sum_j w_tj y_tj in slot order, plus the shared expert's row; empty slots skipped
+template <typename T>
+__global__ __launch_bounds__(256) void mx_combine_kernel(const float *__restrict__ y, const int32_t *__restrict__ idx,
+                                                         const float *__restrict__ w, int T_, int k, int E, int H,
+                                                         int has_shared, T *__restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t t = i / H;
+  const int h = (int)(i - t * H);
+  if (t >= T_) return;
+  v4f s = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < k; j++) {
+    const int64_t p = t * k + j;
+    const int e = idx[p];
+    if (e < 0 || e >= E) continue;
+    s += w[p] * *reinterpret_cast<const v4f *>(y + p * H + h);
+  }
+  if (has_shared) s += *reinterpret_cast<const v4f *>(y + ((int64_t)T_ * k + t) * H + h);
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  v4 o;
+#pragma unroll
+  for (int r = 0; r < 4; r++) o[r] = (T)s[r];
+  *reinterpret_cast<v4 *>(out + i) = o;
+}
+
+hipError_t launch_mx_combine(const float *y, const int32_t *idx, const float *w, int T, int k, int E, int H,
+                             int has_shared, void *out, int dtype, hipStream_t s) {
+  const dim3 g((unsigned)(((int64_t)T * H / 4 + 255) / 256)), b(256);
+  if (dtype == COLI_F32)
+    hipLaunchKernelGGL(mx_combine_kernel<float>, g, b, 0, s, y, idx, w, T, k, E, H, has_shared, (float *)out);
+  else if (dtype == COLI_BF16)
+    hipLaunchKernelGGL(mx_combine_kernel<bf16_t>, g, b, 0, s, y, idx, w, T, k, E, H, has_shared, (bf16_t *)out);
+  else
+    hipLaunchKernelGGL(mx_combine_kernel<f16_t>, g, b, 0, s, y, idx, w, T, k, E, H, has_shared, (f16_t *)out);
+  return hipGetLastError();
+}
+
+}  // namespace coli

@@ -221,6 +221,7 @@ struct RouteLogitsArgs {
   const float *bias;  // null: none
   int32_t *idx;       // [T][k] out
   float *w;           // [T][k] out
+  int m, lshift, vec; // set by the launcher: E / G, log2 of the lanes of a group, whole aligned lanes
 };
 hipError_t launch_route_logits(const RouteLogitsArgs &a, const void *z, int dtype, hipStream_t s);
 

@@ -1,6 +1,8 @@
 // mxfp4_api.hip — the C entry points of the route from logits and of the MXFP4 x MXFP4
 // operators: host-side validation, workspace layout, launches (one stream, no host
 // synchronisation, no device allocation).
+#include <algorithm>
+
 #include "coli_internal.h"
 
 namespace coli {
@@ -76,7 +78,10 @@ static MxArgs expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
 
 static hipError_t launch_experts(MxMode mode, int dtype, MxArgs &a, uint8_t *ws, const MxWs &L, hipStream_t s) {
   a.ws_pitch = a.K / 32;
-  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P) return launch_mx_gemv(mode, dtype, a, s);
+  // the tiled kernel's offsets into the activations and the output have 32 bits
+  const int64_t rows = (int64_t)a.M * (a.k + a.has_shared), widest = std::max<int64_t>((int64_t)a.N * 4, mx_padded(a.K) / 2);
+  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P || rows * widest >= ((int64_t)1 << 32) - 65536)
+    return launch_mx_gemv(mode, dtype, a, s);
   a.tiles = reinterpret_cast<int4 *>(ws + L.tiles);
   a.ntiles = reinterpret_cast<int32_t *>(ws + L.ntiles);
   return launch_mx_tile(mode, dtype, a, s);

@@ -10,7 +10,7 @@
 // under way, which saves a launch.
 //
 // mx_down_kernel: the down product of up to 16 tokens with its weighted combine. A workgroup (8
-// wavefronts) owns 16 output rows of every token and goes through all experts of the route, a
+// wavefronts) owns 8 to 32 output rows of every token and goes through all experts of the route, a
 // token to a column of the matrix instruction; the (expert, K group) units go to the wavefronts
 // in turn. No rows per pair are written, no second kernel sums them.
 #include "mxfp4_impl.h"
@@ -223,17 +223,19 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
 // ------------------------------------------------------------------ down with its combine
 constexpr int DN_TOK = 16, DN_K = 16, DN_WAVES = 8, DN_DEPTH = 2;
 
-template <typename T, MxAct ACT, bool AL16>
-__global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, const int32_t *__restrict__ idx,
+// RT 16-row tiles of the matrix instruction for the `step` output rows of a workgroup: rows past
+// them, like rows past N, read past their buffer's end, which gives zeros without an access.
+template <typename T, MxAct ACT, bool AL16, int RT>
+__global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int step, const int32_t *__restrict__ idx,
                                                                const float *__restrict__ w, T *__restrict__ out) {
   // slots[e * 16 + t]: the slots of token t that hold expert e, a bit each; the experts of the
   // route; ACT_X: the quantised rows
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ float red[DN_WAVES][16][17];
+  __shared__ float red[DN_WAVES][DN_TOK][16 * RT + 1];
   uint16_t *slots = reinterpret_cast<uint16_t *>(lds);
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * step, nrows = min(step, a.N - n0);
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, ng = nbp / 16;
   const int T_ = a.M, k = a.k, E = a.E, P = T_ * k;
   for (int i = tid; i < E * DN_TOK / 2; i += 64 * DN_WAVES) reinterpret_cast<uint32_t *>(slots)[i] = 0;
@@ -265,26 +267,56 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, const 
       if (e >= 0 && e < E) slots[e * DN_TOK + tid] |= (uint16_t)(1u << j);
     }
   __syncthreads();
-  const int wrow = n0 + li;  // N is a multiple of 128
-  const uint8_t *ac = ACT == ACT_X ? lc : a.ac, *as = ACT == ACT_X ? ls : a.as;
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
-  Group wg[DN_DEPTH], act[DN_DEPTH];
+  const int rows = P + a.has_shared * T_;
+  v4f acc[RT] = {};
+  Group wg[DN_DEPTH][RT], act[DN_DEPTH];
   uint32_t held[DN_DEPTH];  // slots of this lane's token that hold a unit's expert
   float wt[DN_DEPTH];       // weight of the first
-  // A token's lanes take the row of slot j of unit (e, g), or any row where there is none.
+  // A token's lanes take the row of its first slot of `mine` that holds expert e. A token without
+  // one (of 16 that pick 8 of 256 experts, 15 have none) reads past the buffer's end: zeros, and
+  // no access to the cache, whose rate this kernel would otherwise meet.
+  [[maybe_unused]] const auto acr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(a.ac), 0, rows * nbp * 16, 0x00027000);
+  [[maybe_unused]] const auto asr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(a.as), 0, rows * nbp, 0x00027000);
+  [[maybe_unused]] const auto wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(w), 0, P * 4, 0x00027000);
   auto load_act = [&](int d, int e, int g, uint32_t mine) {
     const int j = mine ? __builtin_ctz(mine) : 0, p = e < E ? li * k + j : P + li;
-    const int row = mine ? p : (e < E ? 0 : P);
-    load_group<true>(ac + (int64_t)row * nbp * 16, as + (int64_t)row * nbp, nbp, g, lq, act[d]);
-    wt[d] = !mine ? 0.0f : e < E ? w[p] : 1.0f;
+    if constexpr (ACT == ACT_X) {
+      const int row = mine ? p : (e < E ? 0 : P);
+      load_group<true>(lc + row * nbp * 16, ls + row * nbp, nbp, g, lq, act[d]);
+      wt[d] = !mine ? 0.0f : e < E ? w[p] : 1.0f;
+    } else {
+      const uint32_t row = (uint32_t)p * (uint32_t)nbp;
+      const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(asr, mine ? row + g * 16 : ~0u, 0, 0));
+      act[d].u[0] = u.x, act[d].u[1] = u.y, act[d].u[2] = u.z, act[d].u[3] = u.w;
+#pragma unroll
+      for (int s = 0; s < 4; s++)
+        act[d].c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(acr, mine ? (row + g * 16 + 4 * s + lq) * 16 : ~0u, 0, 0));
+      const float v = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(wr, mine && e < E ? p * 4 : ~0u, 0, 0));
+      wt[d] = e < E ? v : 1.0f;
+    }
   };
   // weights and activations of a unit together, since loads arrive in order
   auto load = [&](int d, int u) {
     const int s = u / ng, g = u - s * ng;
     const int e = s < na ? __builtin_amdgcn_readfirstlane(active[s]) : E;
-    const uint8_t *wc = a.wc + (int64_t)e * a.wc_stride + (int64_t)wrow * nb * 16;
-    const uint8_t *ws = a.ws + (int64_t)e * a.ws_stride + (int64_t)wrow * nb;
-    load_group<AL16>(wc, ws, nb, g, lq, wg[d]);
+    const auto wc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(a.wc) + (int64_t)e * a.wc_stride + (int64_t)n0 * nb * 16, 0, nrows * nb * 16, 0x00027000);
+    const auto ws = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(a.ws) + (int64_t)e * a.ws_stride + (int64_t)n0 * nb, 0, nrows * nb, 0x00027000);
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+      const uint32_t row = (uint32_t)(16 * i + li) * (uint32_t)nb;
+      if constexpr (AL16) {
+        const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ws, row + g * 16, 0, 0));
+        wg[d][i].u[0] = u.x, wg[d][i].u[1] = u.y, wg[d][i].u[2] = u.z, wg[d][i].u[3] = u.w;
+      }
+#pragma unroll
+      for (int s = 0; s < 4; s++) {
+        const int b = AL16 ? g * 16 + 4 * s + lq : min(g * 16 + 4 * s + lq, nb - 1);  // past K: activations of zero
+        wg[d][i].c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wc, (row + b) * 16, 0, 0));
+        if constexpr (!AL16) wg[d][i].u[s] = __builtin_amdgcn_raw_buffer_load_b8(ws, row + b, 0, 0);
+      }
+    }
     held[d] = li < T_ ? (e < E ? slots[e * DN_TOK + li] : 1u) : 0u;
     load_act(d, e, g, held[d]);
   };
@@ -298,12 +330,15 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, const 
       if (u < units) {
         uint32_t mine = held[d];
         while (true) {
-          v4f dsum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < 4; s++)  // rows of the result: weight rows; columns: tokens
-            dsum = mx_mfma16(wg[d].c[s], group_scale<AL16>(wg[d], s, lq), act[d].c[s], group_scale<true>(act[d], s, lq), dsum);
+          for (int i = 0; i < RT; i++) {
+            v4f dsum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int r = 0; r < 4; r++) acc[r] = mine ? __builtin_fmaf(wt[d], dsum[r], acc[r]) : acc[r];
+            for (int s = 0; s < 4; s++)  // rows of the result: weight rows; columns: tokens
+              dsum = mx_mfma16(wg[d][i].c[s], group_scale<AL16>(wg[d][i], s, lq), act[d].c[s], group_scale<true>(act[d], s, lq), dsum);
+#pragma unroll
+            for (int r = 0; r < 4; r++) acc[i][r] = mine ? __builtin_fmaf(wt[d], dsum[r], acc[i][r]) : acc[i][r];
+          }
           // a token holds an expert in one slot; a route that repeats one takes another round
           mine &= mine - 1;
           if (__builtin_expect(__ballot(mine != 0) == 0, 1)) break;
@@ -315,15 +350,30 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, const 
     }
   }
 #pragma unroll
-  for (int r = 0; r < 4; r++) red[wv][li][4 * lq + r] = acc[r];
+  for (int i = 0; i < RT; i++)
+#pragma unroll
+    for (int r = 0; r < 4; r++) red[wv][li][16 * i + 4 * lq + r] = acc[i][r];
   __syncthreads();
-  const int t = tid >> 4, r = tid & 15;
-  if (t < T_) {
+  const int t = tid / (16 * RT), r = tid % (16 * RT);
+  if (t < T_ && r < nrows) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < DN_WAVES; i++) s += red[i][t][r];
     out[(int64_t)t * a.N + n0 + r] = (T)s;
   }
+}
+
+// Output rows of a workgroup: so many that the busiest CU has the least to do, a workgroup
+// costing about six rows by itself. N = 6144 in 256 workgroups of 24 rows: every CU the same; in
+// 384 of 16 a third of the CUs' time was idle.
+constexpr int MX_CUS = 256;
+static int down_step(int N) {
+  int best = 16, cost = 1 << 30;
+  for (int step = 8; step <= 32; step += 8) {
+    const int groups = (N + step - 1) / step, c = (groups + MX_CUS - 1) / MX_CUS * (step + 6);
+    if (c < cost) cost = c, best = step;
+  }
+  return best;
 }
 
 // LDS of mx_down_kernel, and of its rows when it quantises them itself
@@ -333,7 +383,8 @@ static size_t down_lds(const MxArgs &a, bool x) {
 }
 
 bool mx_down_fused(const MxArgs &a) { return a.M <= DN_TOK && a.k <= DN_K; }
-bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && down_lds(a, true) <= 56 * 1024; }
+// (the dynamic part of 64 KB; the sums have the rest)
+bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && down_lds(a, true) <= 46 * 1024; }
 // One row quantised by every workgroup
 bool mx_gemv_from_x(const MxArgs &a) { return a.M == 1 && mx_padded(a.K) / 32 * 17 <= 48 * 1024; }
 
@@ -380,17 +431,25 @@ hipError_t launch_mx_gemv(MxMode mode, int dtype, const MxArgs &a, hipStream_t s
 
 template <typename T>
 static hipError_t launch_down_t(const MxArgs &a, const int32_t *idx, const float *w, void *out, hipStream_t s) {
-  const dim3 g((unsigned)(a.N / 16)), b(64 * DN_WAVES);
+  const int step = down_step(a.N);
+  const dim3 g((unsigned)((a.N + step - 1) / step)), b(64 * DN_WAVES);
   const size_t lds = down_lds(a, a.x != nullptr);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, lds, s, a, step, idx, w, (T *)out); };
+  auto pick = [&]<MxAct ACT, bool AL16>() {
+    if (step <= 16)
+      go(mx_down_kernel<T, ACT, AL16, 1>);
+    else
+      go(mx_down_kernel<T, ACT, AL16, 2>);
+  };
   const bool al16 = scales_al16(a);
   if (a.x && al16)
-    hipLaunchKernelGGL((mx_down_kernel<T, ACT_X, true>), g, b, lds, s, a, idx, w, (T *)out);
+    pick.template operator()<ACT_X, true>();
   else if (a.x)
-    hipLaunchKernelGGL((mx_down_kernel<T, ACT_X, false>), g, b, lds, s, a, idx, w, (T *)out);
+    pick.template operator()<ACT_X, false>();
   else if (al16)
-    hipLaunchKernelGGL((mx_down_kernel<T, ACT_WS, true>), g, b, lds, s, a, idx, w, (T *)out);
+    pick.template operator()<ACT_WS, true>();
   else
-    hipLaunchKernelGGL((mx_down_kernel<T, ACT_WS, false>), g, b, lds, s, a, idx, w, (T *)out);
+    pick.template operator()<ACT_WS, false>();
   return hipGetLastError();
 }
 

@@ -86,52 +86,22 @@ __device__ __forceinline__ void tile_of(int id, int nx, int ny, int &x, int &y) 
   x = strip * TILE_STRIP + in - y * w;
 }
 
-// v: four rows of this lane's column -> row q (the lane's place in its quad) of the quad's four
-// columns, rounded to T
-template <typename T>
-__device__ __forceinline__ auto quad_transpose(const float (&v)[4], int q) {
-  auto swap = [](auto x, auto ctrl) {
-    return __builtin_bit_cast(decltype(x), __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, false));
-  };
-  const bool odd = q & 1, up = q & 2;
-  const float s0 = swap(odd ? v[0] : v[1], std::integral_constant<int, 0xB1>{});  // lane ^ 1
-  const float s1 = swap(odd ? v[2] : v[3], std::integral_constant<int, 0xB1>{});
-  typedef T t2 __attribute__((ext_vector_type(2)));
-  typedef T t4 __attribute__((ext_vector_type(4)));
-  // rows q % 2 and 2 + q % 2 of the columns of lanes q & 2, (q & 2) + 1
-  const t2 lo = {(T)(odd ? s0 : v[0]), (T)(odd ? v[1] : s0)};
-  const t2 hi = {(T)(odd ? s1 : v[2]), (T)(odd ? v[3] : s1)};
-  const t2 give = up ? lo : hi, keep = up ? hi : lo;
-  t2 got;
-  if constexpr (sizeof(T) == 2) {
-    got = swap(give, std::integral_constant<int, 0x4E>{});  // lane ^ 2
-  } else {
-    got[0] = swap(give[0], std::integral_constant<int, 0x4E>{});
-    got[1] = swap(give[1], std::integral_constant<int, 0x4E>{});
-  }
-  const t2 l = up ? got : keep, h = up ? keep : got;
-  return t4{l[0], l[1], h[0], h[1]};
-}
-
 template <typename W>
 __device__ __forceinline__ void store_out(W w, __amdgpu_buffer_rsrc_t out, uint32_t off) {
   if constexpr (sizeof(W) == 16)
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, w), out, off, 0, 0);
-  else if constexpr (sizeof(W) == 8)
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, w), out, off, 0, 0);
   else if constexpr (sizeof(W) == 4)
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, w), out, off, 0, 0);
   else
     __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, w), out, off, 0, 0);
 }
 
-// VEC: N is a multiple of 4
-template <MxMode MODE, typename T, typename S, bool VEC>
+// RAGGED: N is no multiple of the columns of a 16-byte piece
+template <MxMode MODE, typename T, typename S, bool RAGGED>
 __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int BM = S::BM, BN = S::BN, MI = S::MI, NI = S::NI, NBUF = S::NBUF, KB = S::KB, KS = S::KS;
   constexpr int BF = MODE == MX_GATEUP ? BN / 2 : BN;  // output columns of a tile
-  static_assert(MODE != MX_GATEUP || NI % 2 == 0, "a wavefront holds gate and up columns");
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / S::WN, wn = wv % S::WN;
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, nst = (nb + KB - 1) / KB;
@@ -148,21 +118,24 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     first = by * BM;
     n = min(BM, a.M - first);
   } else {
-    // Each XCD (id % 8) gets a run of row tiles, all column strips of one after another: the
-    // strips of a row tile share its activations in the XCD's L2, the row tiles of an expert
-    // its weights.
+    // Each XCD (id % 8) gets a run of (group of an expert's row tiles, column strip, row tile),
+    // the row tile fastest: the workgroups that read the same weights run next to each other on
+    // one XCD and share them in its L2; the strips of a group share its activations there.
     const int nt = *a.ntiles, ns = (nx + a.strip - 1) / a.strip, xcd = blockIdx.x & 7, total = nt * ns;
     const int q = total >> 3, r = total & 7, local = blockIdx.x >> 3;
     if (local >= q + (xcd < r)) return;
     const int t = xcd * q + min(xcd, r) + local;
     by = t / ns;
-    bx = (t - by * ns) * a.strip;
+    int4 c = a.tiles[by];
+    const int grp = c.w >> 16, b0 = by - ((c.w >> 8) & 0xFF), in = t - b0 * ns;
+    bx = in / grp * a.strip;
+    by = min(b0 + in % grp, nt - 1);
     cols = min(a.strip, nx - bx);
-    const int4 c = a.tiles[by];
+    c = a.tiles[by];
     e = c.x;
     first = c.y;
     n = c.z;
-    routed = c.w != 0;
+    routed = (c.w & 1) != 0;
   }
   const int64_t P = (int64_t)a.M * a.k;
   // tile row i -> row of the output, of the activations
@@ -185,11 +158,8 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     return MODE == MX_DOWN ? ids[i] : (routed ? ids[i] / a.k : ids[i] - (int)P);
   };
   auto w_row = [&](int r) -> int {  // weight row of column r of the first tile, relative to the base below
-    if constexpr (MODE == MX_GATEUP) {
-      constexpr int WT = BN / S::WN;
-      const int rr = r % WT, m = rr / (WT / 2);
-      return m * a.N + min((r / WT) * (WT / 2) + rr % (WT / 2), a.N - 1 - bx * BF);
-    }
+    if constexpr (MODE == MX_GATEUP)  // by eights: gate rows, then the up rows of the same features
+      return (r >> 3 & 1) * a.N + min((r >> 4) * 8 + (r & 7), a.N - 1 - bx * BF);
     return min(r, a.N - 1 - bx * BF);
   };
   // tile-relative bases keep the lanes' offsets within 32 bits
@@ -316,8 +286,8 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     auto mul = [&](int t, int i, int j) {
       const uint4 x = fa[t & 1][i], y = fb[t & 1][j];
       const uint32_t u = sa[0][i], v = sb[0][j];
-      acc[i][j] = t == 0 ? mx_mfma32<0>(x, u, y, v, acc[i][j]) : t == 1 ? mx_mfma32<1>(x, u, y, v, acc[i][j])
-                : t == 2 ? mx_mfma32<2>(x, u, y, v, acc[i][j]) : mx_mfma32<3>(x, u, y, v, acc[i][j]);
+      acc[i][j] = t == 0 ? mx_mfma32<0>(y, v, x, u, acc[i][j]) : t == 1 ? mx_mfma32<1>(y, v, x, u, acc[i][j])
+                : t == 2 ? mx_mfma32<2>(y, v, x, u, acc[i][j]) : mx_mfma32<3>(y, v, x, u, acc[i][j]);
     };
 
     // While a stage is multiplied the NBUF - 1 after it are on their way. Its last K step is in
@@ -381,43 +351,64 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
         take_scales();
         cur = next;
       }
-      // results: lane column li of a 32 x 32 tile, rows 8 (r / 4) + 4 hh + r % 4. The stores have
-      // no branch (it would bring all results out of the accumulators at once): lanes without a
-      // row or column give an offset past the buffer's end, where a store is dropped.
-      const int c0 = (bx + col) * BF, nleft = a.N - c0;  // columns that exist
-      constexpr int NO = MODE == MX_GATEUP ? NI / 2 : NI;
+      // Results: lane column li (a row of activations) of a 32 x 32 tile, rows (weight rows)
+      // 8 (r / 4) + 4 hh + r % 4, so that a lane holds runs of four output columns. Two bytes to a
+      // value: the halves of the wavefront trade runs and each lane stores eight columns.
+      // The stores have no branch (it would bring all results out of the accumulators at once,
+      // as it does for a ragged N, whose last piece's columns go one by one): lanes without a row,
+      // and pieces past the last column, give an offset past the buffer's end, where a store is
+      // dropped.
+      constexpr int GROUPS = MODE == MX_GATEUP ? 2 : 4, WF = BF / S::WN, JF = MODE == MX_GATEUP ? 16 : 32;
+      typedef T piece_t __attribute__((ext_vector_type(16 / sizeof(T))));
+      constexpr int PC = 16 / sizeof(T);                          // columns of a piece
+      const int left = a.N - (bx + col) * BF - wn * WF;           // columns from the wavefront's first on
+      const bool edge = left < WF;
       int lo = li, ho = hh;
       asm volatile("" : "+v"(lo), "+v"(ho));  // or the stores' offsets would all be kept over the column tiles
 #pragma unroll
-      for (int i = 0; i < MX; i++)
+      for (int i = 0; i < MX; i++) {
+        const int row = wm * (BM / S::WM) + i * 32 + lo;
+        const bool there = row < n;
+        const uint32_t off = ((uint32_t)out_row(row) * (uint32_t)a.N + (bx + col) * BF + wn * WF) * sizeof(T);
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const int row = wm * (BM / S::WM) + i * 32 + 8 * q + 4 * ho;
+        for (int j = 0; j < NI; j++) {
+          auto value = [&](int g, int r) -> T {
+            if constexpr (MODE == MX_GATEUP)
+              return (T)(silu_fast(acc[i][j][8 * g + r]) * acc[i][j][8 * g + 4 + r]);
+            else
+              return (T)acc[i][j][4 * g + r];
+          };
+          auto put = [&](piece_t w, int c) {
+            const uint32_t at = off + c * sizeof(T);
+            store_out(w, out, there && c + PC <= left ? at : ~0u);
+            if (RAGGED && __builtin_expect(edge, 0)) {
 #pragma unroll
-          for (int j = 0; j < NO; j++) {
-            float v[4];
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-              v[r] = acc[i][j][4 * q + r];
-              if constexpr (MODE == MX_GATEUP) v[r] = silu(v[r]) * acc[i][j + NO][4 * q + r];
+              for (int r = 0; r < PC; r++)
+                store_out(w[r], out, there && c + PC > left && c + r < left ? at + r * (int)sizeof(T) : ~0u);
             }
-            const int c = wn * (BF / S::WN) + j * 32 + lo;
-            if constexpr (VEC) {
-              // four columns of one row to a lane: stores of whole 64-byte pieces
-              auto w = quad_transpose<T>(v, lo & 3);
-              const int rr = row + (lo & 3), cc = c & ~3;
-              const uint32_t off = ((uint32_t)out_row(rr) * (uint32_t)a.N + c0 + cc) * sizeof(T);
-              store_out(w, out, rr < n && cc < nleft ? off : ~0u);
-            } else {
+          };
 #pragma unroll
-              for (int r = 0; r < 4; r++) {
-                const uint32_t off = ((uint32_t)out_row(row + r) * (uint32_t)a.N + c0 + c) * sizeof(T);
-                store_out((T)v[r], out, row + r < n && c < nleft ? off : ~0u);
-              }
+          for (int g = 0; g < GROUPS; g += sizeof(T) == 4 ? 1 : 2) {
+            if constexpr (sizeof(T) == 4) {
+              piece_t w;
+#pragma unroll
+              for (int r = 0; r < 4; r++) w[r] = value(g, r);
+              put(w, j * JF + 8 * g + 4 * ho);
+            } else {
+              typedef T half_t __attribute__((ext_vector_type(4)));
+              half_t x, y;
+#pragma unroll
+              for (int r = 0; r < 4; r++) x[r] = value(g, r), y[r] = value(g + 1, r);
+              const v2u32 xu = __builtin_bit_cast(v2u32, x), yu = __builtin_bit_cast(v2u32, y);
+              // the lower lanes get their partner's run of g, the upper ones theirs of g + 1
+              const auto p = __builtin_amdgcn_permlane32_swap(xu[0], yu[0], false, false);
+              const auto q = __builtin_amdgcn_permlane32_swap(xu[1], yu[1], false, false);
+              put(__builtin_bit_cast(piece_t, v4u32{p[0], q[0], p[1], q[1]}), j * JF + 8 * (g + ho));
             }
             __builtin_amdgcn_sched_barrier(0);
           }
         }
+      }
     }
   };
   // routed rows seldom fill a tile: the products of the 32-row tiles that hold none are left out
@@ -434,10 +425,18 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   }
 }
 
-#ifndef STRIP
-#define STRIP 2
-#endif
-// Tiles of a route: {expert, first (of perm, or token), rows, routed}, the shared expert's first.
+// Row tiles of an expert that go through a column strip together (a bit more than one expert's
+// share of a long prompt; more would not fit the L2 with their activations)
+constexpr int EXP_GROUP = 8;
+constexpr int EXP_STRIP = 2;  // column tiles of a workgroup
+
+// Tile c of an expert's `all`: its w entry, routed | place in its group << 8 | size of the group << 16
+__device__ __forceinline__ int tile_place(int c, int all, int routed) {
+  const int i = c % EXP_GROUP;
+  return routed | i << 8 | min(EXP_GROUP, all - (c - i)) << 16;
+}
+
+// Tiles of a route: {expert, first (of perm, or token), rows, place}, the shared expert's first.
 __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap) {
   __shared__ int wsum[16];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -463,10 +462,11 @@ __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap
     if (i < wv) base += wsum[i];
     total += wsum[i];
   }
-  for (int c = tid; c < shared && c < cap; c += 1024) a.tiles[c] = make_int4(a.E, c * bm, min(bm, a.M - c * bm), 0);
+  for (int c = tid; c < shared && c < cap; c += 1024)
+    a.tiles[c] = make_int4(a.E, c * bm, min(bm, a.M - c * bm), tile_place(c, shared, 0));
   int g = base + incl - mine;
   for (int c = 0; c < mine; c++, g++)
-    if (g < cap) a.tiles[g] = make_int4(e, first + c * bm, min(bm, n - c * bm), 1);
+    if (g < cap) a.tiles[g] = make_int4(e, first + c * bm, min(bm, n - c * bm), tile_place(c, mine, 1));
   if (tid == 0) *a.ntiles = min(total, cap);
 }
 
@@ -484,31 +484,25 @@ static int dense_strip(int nx, int ny) {
   return best;
 }
 
-template <MxMode MODE, typename T, typename S, bool VEC = true>
+template <MxMode MODE, typename T, typename S, bool RAGGED = false>
 static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static_assert(S::BYTES <= 160 * 1024, "LDS");
   constexpr int BF = MODE == MX_GATEUP ? S::BN / 2 : S::BN;
-  auto kernel = mx_tile_kernel<MODE, T, S, VEC>;
+  auto kernel = mx_tile_kernel<MODE, T, S, RAGGED>;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (attr != hipSuccess) return attr;
   const int nx = (a.N + BF - 1) / BF;
-  a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny) : STRIP;
+  a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny) : EXP_STRIP;
   const unsigned gx = (unsigned)((nx + a.strip - 1) / a.strip);
   const unsigned groups = gx * (unsigned)ny;
   hipLaunchKernelGGL(kernel, dim3(MODE == MX_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);
   return hipGetLastError();
 }
 
-#ifndef TD
-#define TD 256, 256, 2, 2, 2, 1
-#endif
-#ifndef TE
-#define TE 128, 256, 1, 4, 3, 1
-#endif
-typedef TileShape<TD> TileDense;
-typedef TileShape<TE> TileExperts;
-typedef TileShape<TE, false> TileExpertsShort;  // fewer than 16 blocks in a row
+typedef TileShape<256, 256, 2, 2, 2, 1> TileDense;
+typedef TileShape<128, 256, 1, 4, 3, 1> TileExperts;
+typedef TileShape<128, 256, 1, 4, 3, 1, false> TileExpertsShort;  // fewer than 16 blocks in a row
 
 int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared) {
   const int64_t P = (int64_t)T * k, bm = TileExperts::BM;
@@ -519,7 +513,8 @@ template <typename T>
 static hipError_t launch_tile_t(MxMode mode, const MxArgs &a, hipStream_t s) {
   if (mode == MX_LINEAR) {
     const int ny = (a.M + TileDense::BM - 1) / TileDense::BM;
-    return a.N % 4 == 0 ? launch_tile<MX_LINEAR, T, TileDense>(a, ny, s) : launch_tile<MX_LINEAR, T, TileDense, false>(a, ny, s);
+    return a.N % (16 / sizeof(T)) == 0 ? launch_tile<MX_LINEAR, T, TileDense>(a, ny, s)
+                                       : launch_tile<MX_LINEAR, T, TileDense, true>(a, ny, s);
   }
   const int cap = (int)mx_tile_cap(a.M, a.k, a.E, a.has_shared);
   hipLaunchKernelGGL(mx_plan_kernel, dim3(1), dim3(1024), 0, s, a, TileExperts::BM, cap);

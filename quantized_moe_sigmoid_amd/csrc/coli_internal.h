@@ -229,7 +229,14 @@ hipError_t launch_route_logits(const RouteLogitsArgs &a, const void *z, int dtyp
 constexpr int MX_KSTAGE = 512;
 __host__ __device__ inline int mx_padded(int K) { return (K + MX_KSTAGE - 1) / MX_KSTAGE * MX_KSTAGE; }
 
-constexpr int MX_ROWS_TILE = 127;  // a dense product of more rows takes the tiled kernel
+// A dense product on the tiled kernel? The kernel for few rows takes 0.3 us for 2^20 weights and
+// 64 rows (half that for 32), a workgroup of the tiled one 0.8 us for 256 inputs and, short of
+// filling the CUs, nothing for more rows: they meet at about 64 rows of 10240 outputs. K = 6144:
+// N = 12288, M = 64 28.6 and 22 us, N = 2048, M = 256 21.7 and 25.4, M = 500 36.6 and 25.6.
+__host__ inline bool mx_linear_tiled(int32_t M, int32_t N) {
+  if (M <= 16) return false;
+  return (M <= 32 ? 2 : (M + 63) / 64 * 4) * (int64_t)N > 40960;
+}
 
 enum MxMode { MX_LINEAR, MX_GATEUP, MX_DOWN };
 

@@ -41,7 +41,7 @@ static MxWs mx_ws_down(const coli_moe_cfg &c, int32_t T) {
   return mx_ws(R, c.ffn, mx_tiles(c, T), (size_t)R * c.hidden * sizeof(float));
 }
 static MxWs mx_ws_linear(int32_t M, int32_t N, int32_t K) {
-  return mx_ws(M, K, 0, M > MX_ROWS_TILE ? (size_t)N * (mx_padded(K) / 32) : 0);
+  return mx_ws(M, K, 0, mx_linear_tiled(M, N) ? (size_t)N * (mx_padded(K) / 32) : 0);
 }
 
 static int check_linear(int32_t M, int32_t N, int32_t K) {
@@ -179,7 +179,7 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
     a.x = x;
   else if ((st = mx_dev(launch_mx_quantize_rows(x, dtype, M, K, ws + L.ac, ws + L.as, s))))
     return st;
-  if (M <= MX_ROWS_TILE) return mx_dev(launch_mx_gemv(MX_LINEAR, dtype, a, s));
+  if (!mx_linear_tiled(M, N)) return mx_dev(launch_mx_gemv(MX_LINEAR, dtype, a, s));
   if (K % 128 || K < 512 || !mx_aligned(scales, 4)) {  // the tiled kernel loads 16 scales at a dword's address
     if ((st = mx_dev(launch_mx_pad_scales(scales, N, K, ws + L.y, s)))) return st;
     a.ws = ws + L.y;

@@ -9,10 +9,12 @@
 // activations (x in ACT_X) is quantised by every workgroup itself while its first weights are
 // under way, which saves a launch.
 //
-// mx_down_kernel: the down product of up to 16 tokens with its weighted combine. A workgroup (8
+// mx_down_kernel: the down product of few tokens (16 to a workgroup) with its weighted combine. A workgroup (8
 // wavefronts) owns 8 to 32 output rows of every token and goes through all experts of the route, a
 // token to a column of the matrix instruction; the (expert, K group) units go to the wavefronts
 // in turn. No rows per pair are written, no second kernel sums them.
+#include <cmath>
+
 #include "mxfp4_impl.h"
 
 namespace coli {
@@ -237,11 +239,11 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
   const int li = lane & 15, lq = lane >> 4;
   const int n0 = blockIdx.x * step, nrows = min(step, a.N - n0);
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, ng = nbp / 16;
-  const int T_ = a.M, k = a.k, E = a.E, P = T_ * k;
+  const int t0 = blockIdx.y * DN_TOK, T_ = min(DN_TOK, a.M - t0);  // this workgroup's tokens
+  const int k = a.k, E = a.E, P = a.M * k;
   for (int i = tid; i < E * DN_TOK / 2; i += 64 * DN_WAVES) reinterpret_cast<uint32_t *>(slots)[i] = 0;
   int *active = reinterpret_cast<int *>(lds + E * DN_TOK * 2);
-  const int na = max(0, min(*a.nact, E)), units = (na + a.has_shared) * ng;
-  for (int i = tid; i < na; i += 64 * DN_WAVES) active[i] = a.active[i];
+  __shared__ int n_active;
   uint8_t *lc = lds + (E * (DN_TOK * 2 + 4) + 15) / 16 * 16, *ls = lc;
   if constexpr (ACT == ACT_X) {
     ls = lc + (P + a.has_shared) * nbp * 16;
@@ -263,11 +265,25 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
   __syncthreads();
   if (tid < T_)
     for (int j = 0; j < k; j++) {
-      const int e = idx[tid * k + j];
+      const int e = idx[(t0 + tid) * k + j];
       if (e >= 0 && e < E) slots[e * DN_TOK + tid] |= (uint16_t)(1u << j);
     }
   __syncthreads();
-  const int rows = P + a.has_shared * T_;
+  if (wv == 0) {  // the experts that these tokens hold, in order
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = min(e0 + lane, E - 1);
+      const uint4 x = reinterpret_cast<const uint4 *>(slots)[2 * e], y = reinterpret_cast<const uint4 *>(slots)[2 * e + 1];
+      const bool held = e0 + lane < E && (x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
+      const uint64_t who = __ballot(held);
+      if (held) active[n + __popcll(who & ((1ull << lane) - 1))] = e;
+      n += __popcll(who);
+    }
+    if (lane == 0) n_active = n;
+  }
+  __syncthreads();
+  const int na = n_active, units = (na + a.has_shared) * ng;
+  const int rows = P + a.has_shared * a.M;
   v4f acc[RT] = {};
   Group wg[DN_DEPTH][RT], act[DN_DEPTH];
   uint32_t held[DN_DEPTH];  // slots of this lane's token that hold a unit's expert
@@ -279,7 +295,7 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
   [[maybe_unused]] const auto asr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(a.as), 0, rows * nbp, 0x00027000);
   [[maybe_unused]] const auto wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(w), 0, P * 4, 0x00027000);
   auto load_act = [&](int d, int e, int g, uint32_t mine) {
-    const int j = mine ? __builtin_ctz(mine) : 0, p = e < E ? li * k + j : P + li;
+    const int j = mine ? __builtin_ctz(mine) : 0, p = e < E ? (t0 + li) * k + j : P + t0 + li;
     if constexpr (ACT == ACT_X) {
       const int row = mine ? p : (e < E ? 0 : P);
       load_group<true>(lc + row * nbp * 16, ls + row * nbp, nbp, g, lq, act[d]);
@@ -359,7 +375,7 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < DN_WAVES; i++) s += red[i][t][r];
-    out[(int64_t)t * a.N + n0 + r] = (T)s;
+    out[(int64_t)(t0 + t) * a.N + n0 + r] = (T)s;
   }
 }
 
@@ -382,7 +398,17 @@ static size_t down_lds(const MxArgs &a, bool x) {
   return ((size_t)a.E * (DN_TOK * 2 + 4) + 15) / 16 * 16 + (x ? ((size_t)a.M * a.k + (size_t)a.M * a.has_shared) * nbp * 17 : 0);
 }
 
-bool mx_down_fused(const MxArgs &a) { return a.M <= DN_TOK && a.k <= DN_K; }
+// More than 16 tokens go through the weights of their experts once for each 16: worth it while
+// that reads less than 1.7 times the distinct experts of an even route. Of 256 experts of
+// 6144 x 2048, 8 to a token: 24 tokens 267 -> 188 us, 32 323 -> 237 (1.27 times), 48 398 -> 354
+// (1.55 times); 64 (1.85 times) about 450 against 438.
+bool mx_down_fused(const MxArgs &a) {
+  if (a.k > DN_K) return false;
+  if (a.M <= DN_TOK) return true;
+  if (a.M > 4 * DN_TOK) return false;
+  auto hit = [&](int tokens) { return 1.0 - std::pow(1.0 - (double)a.k / a.E, tokens); };
+  return a.M / DN_TOK * hit(DN_TOK) + hit(a.M % DN_TOK) <= 1.7 * hit(a.M);
+}
 // (the dynamic part of 64 KB; the sums have the rest)
 bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && down_lds(a, true) <= 46 * 1024; }
 // One row quantised by every workgroup
@@ -432,7 +458,7 @@ hipError_t launch_mx_gemv(MxMode mode, int dtype, const MxArgs &a, hipStream_t s
 template <typename T>
 static hipError_t launch_down_t(const MxArgs &a, const int32_t *idx, const float *w, void *out, hipStream_t s) {
   const int step = down_step(a.N);
-  const dim3 g((unsigned)((a.N + step - 1) / step)), b(64 * DN_WAVES);
+  const dim3 g((unsigned)((a.N + step - 1) / step), (unsigned)((a.M + DN_TOK - 1) / DN_TOK)), b(64 * DN_WAVES);
   const size_t lds = down_lds(a, a.x != nullptr);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, lds, s, a, step, idx, w, (T *)out); };
   auto pick = [&]<MxAct ACT, bool AL16>() {

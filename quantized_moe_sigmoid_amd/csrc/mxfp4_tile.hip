@@ -411,11 +411,12 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
       }
     }
   };
-  // routed rows seldom fill a tile: the products of the 32-row tiles that hold none are left out
-  if constexpr (MODE == MX_LINEAR) {
+  // routed rows and short batches seldom fill a tile: the products of the 32-row tiles that hold
+  // none are left out
+  if constexpr (S::WM > 1) {
     run.template operator()<MI>();
   } else {
-    static_assert(S::WM == 1 && MI == 4);
+    static_assert(MI == 4);
     if (n <= 32)
       run.template operator()<1>();
     else if (n <= 64)
@@ -470,15 +471,15 @@ __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap
   if (tid == 0) *a.ntiles = min(total, cap);
 }
 
-// Column tiles of a dense workgroup: one workgroup runs on a CU at a time, and a strip's start
-// and end cost about a third of a tile.
+// Column tiles of a dense workgroup: `slots` workgroups run at a time, and a strip's start and
+// end cost about a third of a tile.
 constexpr int MX_CUS = 256;
-static int dense_strip(int nx, int ny) {
+static int dense_strip(int nx, int ny, int slots) {
   int best = 1;
   double cost = 1e300;
   for (int s = 1; s <= 8 && s <= nx; s++) {
     const int64_t groups = (int64_t)((nx + s - 1) / s) * ny;
-    const double c = (double)((groups + MX_CUS - 1) / MX_CUS) * (s + 0.33);
+    const double c = (double)((groups + slots - 1) / slots) * (s + 0.33);
     if (c < cost) cost = c, best = s;
   }
   return best;
@@ -493,7 +494,7 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
       hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (attr != hipSuccess) return attr;
   const int nx = (a.N + BF - 1) / BF;
-  a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny) : EXP_STRIP;
+  a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny, MX_CUS * S::OCC) : EXP_STRIP;
   const unsigned gx = (unsigned)((nx + a.strip - 1) / a.strip);
   const unsigned groups = gx * (unsigned)ny;
   hipLaunchKernelGGL(kernel, dim3(MODE == MX_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);
@@ -501,6 +502,10 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
 }
 
 typedef TileShape<256, 256, 2, 2, 2, 1> TileDense;
+typedef TileShape<128, 128, 1, 4, 2, 2> TileDenseSmall;
+// Fewer big tiles than this leave too many CUs without work. K = 6144, N = 12288: 26 us against 49
+// with 48 big tiles (M = 256), 61 against 57 with 192; K = 2048, N = 4096: 20 against 27 with 128.
+constexpr int DENSE_BIG_TILES = 192;
 typedef TileShape<128, 256, 1, 4, 3, 1> TileExperts;
 typedef TileShape<128, 256, 1, 4, 3, 1, false> TileExpertsShort;  // fewer than 16 blocks in a row
 
@@ -512,9 +517,13 @@ int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared) {
 template <typename T>
 static hipError_t launch_tile_t(MxMode mode, const MxArgs &a, hipStream_t s) {
   if (mode == MX_LINEAR) {
-    const int ny = (a.M + TileDense::BM - 1) / TileDense::BM;
-    return a.N % (16 / sizeof(T)) == 0 ? launch_tile<MX_LINEAR, T, TileDense>(a, ny, s)
-                                       : launch_tile<MX_LINEAR, T, TileDense, true>(a, ny, s);
+    auto go = [&]<typename S>() {
+      const int ny = (a.M + S::BM - 1) / S::BM;
+      return a.N % (16 / sizeof(T)) == 0 ? launch_tile<MX_LINEAR, T, S>(a, ny, s)
+                                         : launch_tile<MX_LINEAR, T, S, true>(a, ny, s);
+    };
+    const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+    return tiles >= DENSE_BIG_TILES ? go.template operator()<TileDense>() : go.template operator()<TileDenseSmall>();
   }
   const int cap = (int)mx_tile_cap(a.M, a.k, a.E, a.has_shared);
   hipLaunchKernelGGL(mx_plan_kernel, dim3(1), dim3(1024), 0, s, a, TileExperts::BM, cap);

@@ -425,3 +425,134 @@ def test_refused_tensors(q):
     assert e.value.status == q.COLI_E_WORKSPACE
     with pytest.raises(TypeError):
         q.mxfp4_linear(x, c, s, torch.zeros((4, 4), device="cuda", dtype=torch.bfloat16), ws)
+
+
+# ------------------------------------------------------------------ sizes of the tiled kernels
+TILED = [  # 128 x 128 tiles: several strips, odd N, short rows; then 256 x 256 ones
+    (33, 10300, 96), (40, 11003, 544), (129, 3500, 288), (300, 2304, 640), (257, 2101, 1024), (513, 1300, 1312),
+    (1025, 9801, 320), (2048, 6144, 128)]
+
+
+@pytest.mark.parametrize("M,N,K", TILED)
+@pytest.mark.parametrize("dtype", DT)
+def test_linear_tiled(q, M, N, K, dtype):
+    print(f"linear M={M} N={N} K={K} {dtype}", flush=True)
+    _check_linear(q, M, N, K, dtype, M + N + K)
+
+
+def test_linear_writes_its_output_alone(q):
+    """Rows that end inside a 16-byte piece: neighbours of the output keep what they held."""
+    import torch
+    for M, N in ((5, 13), (300, 2305), (200, 3507)):
+        K = 96
+        rng = np.random.default_rng(N)
+        buf = torch.full((64 + M * N + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[64:64 + M * N].view(M, N)
+        wc, wsc = _weights(rng, N, K)
+        x = _t(rng.standard_normal((M, K)).astype(np.float32), "bfloat16")
+        q.mxfp4_linear(x, _t(wc), _t(wsc), out, q.alloc_mxfp4_linear_workspace(M, N, K))
+        assert (buf[:64] == 5).all() and (buf[64 + M * N:] == 5).all()
+
+
+def test_linear_unaligned_scales(q):
+    """Scale bytes at any address, for both kernels."""
+    import torch
+    for M, N, K in ((1, 40, 512), (20, 40, 1024), (300, 2304, 640)):
+        rng = np.random.default_rng(K)
+        wc, wsc = _weights(rng, N, K)
+        x = _t(rng.standard_normal((M, K)).astype(np.float32))
+        want, got = (torch.empty((M, N), device="cuda") for _ in range(2))
+        ws = q.alloc_mxfp4_linear_workspace(M, N, K)
+        q.mxfp4_linear(x, _t(wc), _t(wsc), want, ws)
+        off = torch.zeros(wsc.size + 1, dtype=torch.uint8, device="cuda")
+        off[1:] = _t(wsc).flatten()
+        q.mxfp4_linear(x, _t(wc), off[1:].view(N, K // 32), got, ws)
+        assert torch.equal(got, want)
+
+
+EXPERTS_MORE = [
+    (20, 640, 512, 64, 1, True, 0, False),       # down of two blocks of 16 tokens
+    (48, 384, 256, 256, 8, True, 0.2, False),    # three, the experts of each its own
+    (33, 256, 640, 128, 2, False, 0, True),      # a last block of one token
+    (1200, 256, 128, 4, 2, True, 0, False),      # more row tiles of an expert than go together
+    (5, 2048, 384, 16, 2, True, 0, False),       # 8 down rows to a workgroup, K = 3 * 128
+    (3, 5248, 128, 8, 2, False, 0, False),       # 24 rows, the last workgroup short
+]
+
+
+@pytest.mark.parametrize("case", EXPERTS_MORE, ids=str)
+@pytest.mark.parametrize("dtype", DT)
+def test_gate_up_more(q, case, dtype):
+    test_gate_up(q, case, dtype)
+
+
+@pytest.mark.parametrize("case", EXPERTS_MORE, ids=str)
+@pytest.mark.parametrize("dtype", DT)
+def test_down_more(q, case, dtype):
+    test_down(q, case, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 16, 40])
+def test_gate_up_extremes(q, T):
+    """Gates far from 0, both signs: silu is g or 0 there, never NaN."""
+    import torch
+    H, F, E, k = 256, 128, 4, 2
+    cfg = q.make_cfg(H, F, E, k, has_shared=False, wbits=q.W_MXFP4, scale_group=32)
+    codes = np.full((E, 3, F * H // 2), 0x22, np.uint8)           # every weight 1 ..
+    codes[:, 0, F * H // 4:] = 0xAA                               # .. the gate's upper half -1
+    scales = np.full((E, 3, F * H // 32), 127, np.uint8)
+    idx = np.tile(np.array([[0, 3]], np.int32), (T, 1))
+    grouping = [_t(a) for a in (lambda p, o, a, n: (o, p, a, n))(*mxref.group(idx, E))]
+    w = q.Weights(_t(codes.reshape(E, -1)), _t(scales.reshape(E, -1)), None, None)
+    h = torch.empty((T * k, F), device="cuda")
+    for v in (1.0, 64.0, 2.0 ** 40, 2.0 ** 60):
+        x = torch.full((T, H), v, device="cuda")
+        q.mxfp4_gate_up(cfg, w, x, *grouping, h, q.alloc_mxfp4_experts_workspace(cfg, T))
+        got = _n(h)
+        # e^-256 is nothing beside 1; past fp32's largest (2^128) the rounded value is inf
+        want = (v * H) ** 2 if (v * H) ** 2 < 2.0 ** 128 else np.inf
+        assert np.array_equal(got[:, :F // 2], np.full((T * k, F // 2), want)), v
+        assert (np.abs(got[:, F // 2:]) <= 2.0 ** -120).all(), v                            # -256 v e^(-256 v) 256 v
+
+
+def test_layer_on_side_stream_with_reused_workspace(q):
+    """Two layers one after another on a stream of their own, with one workspace and outputs that
+    another stream wrote before: the second equals a fresh run."""
+    import torch
+    case = (70, 256, 384, 8, 3, True, 0.1, False)
+    rng, cfg, weights, idx, w, grouping, _, _ = _setup(q, case, 77)
+    T, H, F, k = 70, 256, 384, 3
+    x = _t(rng.standard_normal((T, H)).astype(np.float32), "bfloat16")
+    it, wt = _t(idx), _t(w)
+
+    def layer(ws):
+        h = torch.zeros((T * (k + 1), F), dtype=torch.bfloat16, device="cuda")
+        out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        q.mxfp4_gate_up(cfg, weights, x, *grouping, h, ws)
+        q.mxfp4_down(cfg, weights, h, it, wt, *grouping, out, ws)
+        return out
+
+    want = layer(q.alloc_mxfp4_experts_workspace(cfg, T))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ws = q.alloc_mxfp4_experts_workspace(cfg, 100)
+        outs = [layer(ws) for _ in range(3)]
+    s.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_down_token_blocks_bitidentical(q):
+    """A token's down row does not depend on the tokens beside it while both calls take 16 at a time."""
+    import torch
+    case = (20, 640, 512, 64, 2, True, 0, False)
+    T, H, F, E, k = case[:5]
+    rng, cfg, weights, idx, w, grouping, _, _ = _setup(q, case, 9)
+    h = _t(rng.standard_normal((T * (k + 1), F)).astype(np.float32))
+    out, one = torch.empty((T, H), device="cuda"), torch.empty((4, H), device="cuda")
+    ws = q.alloc_mxfp4_experts_workspace(cfg, T)
+    q.mxfp4_down(cfg, weights, h, _t(idx), _t(w), *grouping, out, ws)
+    rows = torch.cat([h[16 * k:20 * k], h[T * k + 16:]]).contiguous()  # the last four tokens alone
+    perm, off, act, na = mxref.group(idx[16:], E)
+    q.mxfp4_down(cfg, weights, rows, _t(idx[16:]), _t(w[16:]), *[_t(a) for a in (off, perm, act, na)], one, ws)
+    assert torch.equal(out[16:], one)

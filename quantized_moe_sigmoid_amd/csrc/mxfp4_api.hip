@@ -44,9 +44,14 @@ static MxWs mx_ws_linear(int32_t M, int32_t N, int32_t K) {
   return mx_ws(M, K, 0, mx_linear_tiled(M, N) ? (size_t)N * (mx_padded(K) / 32) : 0);
 }
 
+// Blocks of 32 of one launch: two threads each, of fewer than 2^32
+constexpr int64_t MX_MAX_BLOCKS = ((int64_t)1 << 31) - 128;
+
 static int check_linear(int32_t M, int32_t N, int32_t K) {
   if (M < 0 || N < 0 || K <= 0) return COLI_E_INVALID;
   if (K % 32 || K > (1 << 20) || M > (1 << 20) || N > (1 << 20)) return COLI_E_UNSUPPORTED;
+  const int64_t nbp = mx_padded(K) / 32;
+  if (M * nbp > MX_MAX_BLOCKS || N * nbp > 4 * MX_MAX_BLOCKS) return COLI_E_UNSUPPORTED;
   return COLI_OK;
 }
 
@@ -126,7 +131,7 @@ int coli_moe_route_logits(const coli_moe_router *r, const void *z, int dtype, in
 
 static int check_mx_rows(const void *x, int dtype, int64_t rows, int32_t cols, const void *codes, const void *scales) {
   if (rows < 0 || cols <= 0 || !mx_dtype(dtype)) return COLI_E_INVALID;
-  if (cols % 32 || rows > ((int64_t)1 << 31) / (cols / 32)) return COLI_E_UNSUPPORTED;  // blocks of one launch
+  if (cols % 32 || rows > MX_MAX_BLOCKS / (cols / 32)) return COLI_E_UNSUPPORTED;
   if (rows == 0) return COLI_OK;
   if (!x || !codes || !scales) return COLI_E_INVALID;
   if (!mx_aligned(x, 16) || !mx_aligned(codes, 16)) return COLI_E_ALIGN;

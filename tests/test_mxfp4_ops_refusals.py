@@ -144,3 +144,14 @@ def test_definition_of_route_against_sort():
     idx, w = mxref.route(z, 5)
     assert np.array_equal(idx, np.argsort(-z, axis=1, kind="stable")[:, :5])
     assert np.allclose(w.sum(1), 1)
+
+
+def test_sizes_beyond_one_launch(q):
+    """Products and conversions whose blocks of 32 pass what one launch counts are refused, not truncated."""
+    L = q.lib()
+    assert L.coli_moe_mxfp4_quantize(P, 0, 1 << 31, 32, P, P, None) == -2
+    assert L.coli_moe_mxfp4_dequantize(P, P, (1 << 31) - 127, 32, P, 1, None) == -2
+    assert L.coli_moe_mxfp4_linear_workspace_bytes(1 << 20, 16, 1 << 20) == 0
+    assert L.coli_moe_mxfp4_linear_workspace_bytes(16, 1 << 20, 1 << 20) == 0
+    assert L.coli_moe_mxfp4_linear(P, 0, P, P, 1 << 20, 16, 1 << 20, P, P, 1 << 62, None) == -2
+    assert L.coli_moe_mxfp4_linear_workspace_bytes(1 << 20, 16, 1 << 15) > 0

@@ -7,12 +7,16 @@
 // contiguous bytes of a row) in turn, two groups of weights under way at a time straight into
 // the operand registers; their sums meet in LDS, added in wavefront order. One row of
 // activations (x in ACT_X) is quantised by every workgroup itself while its first weights are
-// under way, which saves a launch.
+// under way, which saves a launch. One token, bf16: dense 12288 x 6144 8.3 to 9 us (40 MB, 6.4 us
+// at the 6.3 TB/s of a plain streaming read, and a launch), gate/up of 9 experts of 6144 x 2048
+// 24.5 us (120 MB, 4.9 TB/s); gate/up of 16 tokens over 256 experts 243 us (5.7 TB/s).
 //
-// mx_down_kernel: the down product of few tokens (16 to a workgroup) with its weighted combine. A workgroup (8
-// wavefronts) owns 8 to 32 output rows of every token and goes through all experts of the route, a
-// token to a column of the matrix instruction; the (expert, K group) units go to the wavefronts
-// in turn. No rows per pair are written, no second kernel sums them.
+// mx_down_kernel: the down product of few tokens (16 to a workgroup) with its weighted combine. A
+// workgroup (8 wavefronts) owns 8 to 32 output rows of its tokens and goes through all experts
+// they hold, a token to a column of the matrix instruction; the (expert, K group) units go to the
+// wavefronts in turn, two of each under way. No rows per pair are written, no second kernel sums
+// them. 16 tokens over 256 experts of 6144 x 2048: 118 us with the quantisation of h, 112 of them
+// this kernel (0.69 GB, 6.1 TB/s: the rate of a plain read). Three units under way: the same.
 #include <cmath>
 
 #include "mxfp4_impl.h"
@@ -26,29 +30,50 @@ struct Group {
   uint32_t u[4];
 };
 
-// Group g of a row of nb blocks; AL16: nb is a multiple of 16 and the scales are 16-byte aligned
-template <bool AL16>
+// How a row's scales come in: SC_FULL: nb is a multiple of 16 and the scales are 16-byte aligned;
+// SC_ANY: 16 bytes at any address, nb >= 16 (a group that the row ends in takes the row's last 16,
+// shifted at the product); SC_BYTES: byte by byte, for shorter rows. 16 tokens of 64 experts,
+// K = 1920: gate/up 95 us with byte loads.
+enum ScaleLoad { SC_FULL, SC_ANY, SC_BYTES };
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
+template <ScaleLoad SL>
 __device__ __forceinline__ void load_group(const uint8_t *codes, const uint8_t *scales, int nb, int g, int lq, Group &o) {
-  if constexpr (AL16) {
+  if constexpr (SL == SC_FULL) {
     const uint4 u = *reinterpret_cast<const uint4 *>(scales + g * 16);
     o.u[0] = u.x, o.u[1] = u.y, o.u[2] = u.z, o.u[3] = u.w;  // shifted at the product
+  } else if constexpr (SL == SC_ANY) {
+    const u32x4_any u = *reinterpret_cast<const u32x4_any *>(scales + min(g * 16, nb - 16));
+    o.u[0] = u[0], o.u[1] = u[1], o.u[2] = u[2], o.u[3] = u[3];
   }
 #pragma unroll
   for (int s = 0; s < 4; s++) {
     const int b = g * 16 + 4 * s + lq;
-    if constexpr (AL16) {
-      o.c[s] = *reinterpret_cast<const uint4 *>(codes + b * 16);
-    } else {
-      const int bb = min(b, nb - 1);  // past the row: the last block; it meets activations of zero
-      o.c[s] = *reinterpret_cast<const uint4 *>(codes + bb * 16);
-      o.u[s] = scales[bb];
+    const int bb = SL == SC_FULL ? b : min(b, nb - 1);  // past the row: the last block; it meets activations of zero
+    o.c[s] = *reinterpret_cast<const uint4 *>(codes + bb * 16);
+    if constexpr (SL == SC_BYTES) o.u[s] = scales[bb];
+  }
+}
+
+// SC_ANY, before the products: the group that the row ends in, of which the last 16 scales came
+template <ScaleLoad SL>
+__device__ __forceinline__ void end_group(Group &o, int nb, int g) {
+  if constexpr (SL == SC_ANY) {
+    const int past = g * 16 + 16 - nb;  // bytes that came too early; what moves in behind is a scale of the row or 0
+    if (past > 0) {
+      for (int i = past >> 2; i > 0; i--) o.u[0] = o.u[1], o.u[1] = o.u[2], o.u[2] = o.u[3];
+      const uint32_t r = past & 3;
+      o.u[0] = __builtin_amdgcn_alignbyte(o.u[1], o.u[0], r);
+      o.u[1] = __builtin_amdgcn_alignbyte(o.u[2], o.u[1], r);
+      o.u[2] = __builtin_amdgcn_alignbyte(o.u[3], o.u[2], r);
+      o.u[3] >>= 8 * r;
     }
   }
 }
 
-template <bool AL16>
+template <ScaleLoad SL>
 __device__ __forceinline__ uint32_t group_scale(const Group &g, int s, int lq) {
-  return AL16 ? g.u[s] >> (8 * lq) : g.u[s];
+  return SL == SC_BYTES ? g.u[s] : g.u[s] >> (8 * lq);
 }
 
 // One row x of nb blocks -> codes and scales in LDS (blocks nb .. nbp: zeros), by 256 threads.
@@ -93,16 +118,26 @@ __device__ __forceinline__ void quantise_x(const T *x, int nb, int nbp, int tid,
 
 enum MxAct { ACT_WS, ACT_X };  // activations: quantised in the workspace; one row of x
 
-template <MxMode MODE, typename T, int NT, MxAct ACT, bool AL16>
+// Gate and up rows of a product of one token (and of rows without whole aligned groups, whose
+// loads need more registers) share a tile of the matrix instruction, eight of each, which takes
+// half the registers; else a workgroup has 16 of each: over 16 tokens 244 us against 265, over
+// one 25.2 and 25.0.
+template <MxMode MODE, MxAct ACT, ScaleLoad SL>
+constexpr bool gate_up_halves() {
+  return MODE == MX_GATEUP && (ACT == ACT_X || SL != SC_FULL);
+}
+
+template <MxMode MODE, typename T, int NT, MxAct ACT, ScaleLoad SL>
 __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
-  constexpr int NMAT = MODE == MX_GATEUP ? 2 : 1;
+  constexpr bool HALVES = gate_up_halves<MODE, ACT, SL>();
+  constexpr int NMAT = MODE == MX_GATEUP && !HALVES ? 2 : 1;
   constexpr int D = NT == 4 ? 1 : 2;  // groups under way: what the registers hold
   static_assert(ACT == ACT_WS || (NT == 1 && MODE != MX_DOWN));
   extern __shared__ __align__(16) uint8_t lds[];  // ACT_X: the quantised row
   __shared__ float red[4][NMAT][NT][16][17];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * (HALVES ? 8 : 16);
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32;
   const int ngw = (nbp / 16 - wv + 3) / 4;  // groups of this wavefront: wv, wv + 4, ..
   // the rows of activations: first .. first + n - 1 of perm (routed) or of the tokens
@@ -133,7 +168,7 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
   const uint8_t *wc[NMAT], *ws[NMAT];
 #pragma unroll
   for (int m = 0; m < NMAT; m++) {
-    const int64_t row = (int64_t)m * a.N + min(n0 + li, a.N - 1);
+    const int64_t row = HALVES ? (int64_t)(li >> 3) * a.N + min(n0 + (li & 7), a.N - 1) : (int64_t)m * a.N + min(n0 + li, a.N - 1);
     wc[m] = a.wc + (int64_t)e * a.wc_stride + row * nb * 16;
     ws[m] = a.ws + (int64_t)e * a.ws_stride + row * nb;
   }
@@ -157,11 +192,11 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
     // loads arrive in order
     auto load_act = [&](int d, int i) {
 #pragma unroll
-      for (int q = 0; q < NT; q++) load_group<true>(ac[q], as[q], nbp, wv + 4 * i, lq, act[d][q]);
+      for (int q = 0; q < NT; q++) load_group<SC_FULL>(ac[q], as[q], nbp, wv + 4 * i, lq, act[d][q]);
     };
     auto load = [&](int d, int i) {
 #pragma unroll
-      for (int m = 0; m < NMAT; m++) load_group<AL16>(wc[m], ws[m], nb, wv + 4 * i, lq, w[d][m]);
+      for (int m = 0; m < NMAT; m++) load_group<SL>(wc[m], ws[m], nb, wv + 4 * i, lq, w[d][m]);
       if constexpr (ACT == ACT_WS) load_act(d, i);
     };
 #pragma unroll
@@ -180,13 +215,15 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
         if (i0 + d < ngw) {
           if constexpr (ACT == ACT_X) load_act(d, i0 + d);
 #pragma unroll
+          for (int m = 0; m < NMAT; m++) end_group<SL>(w[d][m], nb, wv + 4 * (i0 + d));
+#pragma unroll
           for (int s = 0; s < 4; s++)
 #pragma unroll
             for (int q = 0; q < NT; q++)
 #pragma unroll
               for (int m = 0; m < NMAT; m++)
-                acc[q][m] = mx_mfma16(act[d][q].c[s], group_scale<true>(act[d][q], s, lq), w[d][m].c[s],
-                                      group_scale<AL16>(w[d][m], s, lq), acc[q][m]);
+                acc[q][m] = mx_mfma16(act[d][q].c[s], group_scale<SC_FULL>(act[d][q], s, lq), w[d][m].c[s],
+                                      group_scale<SL>(w[d][m], s, lq), acc[q][m]);
           if (i0 + d + D < ngw) load(d, i0 + d + D);
         }
       }
@@ -201,21 +238,20 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
     const int tr = tid >> 4, tc = tid & 15;
 #pragma unroll
     for (int q = 0; q < NT; q++) {
-      float v[NMAT];
-#pragma unroll
-      for (int m = 0; m < NMAT; m++)
-        v[m] = ((red[0][m][q][tr][tc] + red[1][m][q][tr][tc]) + red[2][m][q][tr][tc]) + red[3][m][q][tr][tc];
+      auto sum = [&](int m, int col) {
+        return ((red[0][m][q][tr][col] + red[1][m][q][tr][col]) + red[2][m][q][tr][col]) + red[3][m][q][tr][col];
+      };
       const int row = c + 16 * q + tr;
-      if (row < n && n0 + tc < a.N) {
+      if (row < n && n0 + tc < a.N && (!HALVES || tc < 8)) {
         const int ci = first + row;
         const int64_t orow = MODE == MX_LINEAR ? ci : (routed ? (int64_t)a.perm[ci] : P + ci);
         const int64_t o = orow * a.N + n0 + tc;
         if constexpr (MODE == MX_GATEUP)
-          static_cast<T *>(a.out)[o] = (T)(silu(v[0]) * v[1]);
+          static_cast<T *>(a.out)[o] = (T)(silu(sum(0, tc)) * (HALVES ? sum(0, tc + 8) : sum(NMAT - 1, tc)));
         else if constexpr (MODE == MX_DOWN)
-          static_cast<float *>(a.out)[o] = v[0];
+          static_cast<float *>(a.out)[o] = sum(0, tc);
         else
-          static_cast<T *>(a.out)[o] = (T)v[0];
+          static_cast<T *>(a.out)[o] = (T)sum(0, tc);
       }
     }
     if (c + 16 * NT < n) __syncthreads();
@@ -227,7 +263,7 @@ constexpr int DN_TOK = 16, DN_K = 16, DN_WAVES = 8, DN_DEPTH = 2;
 
 // RT 16-row tiles of the matrix instruction for the `step` output rows of a workgroup: rows past
 // them, like rows past N, read past their buffer's end, which gives zeros without an access.
-template <typename T, MxAct ACT, bool AL16, int RT>
+template <typename T, MxAct ACT, ScaleLoad SL, int RT>
 __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int step, const int32_t *__restrict__ idx,
                                                                const float *__restrict__ w, T *__restrict__ out) {
   // slots[e * 16 + t]: the slots of token t that hold expert e, a bit each; the experts of the
@@ -298,7 +334,7 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
     const int j = mine ? __builtin_ctz(mine) : 0, p = e < E ? (t0 + li) * k + j : P + t0 + li;
     if constexpr (ACT == ACT_X) {
       const int row = mine ? p : (e < E ? 0 : P);
-      load_group<true>(lc + row * nbp * 16, ls + row * nbp, nbp, g, lq, act[d]);
+      load_group<SC_FULL>(lc + row * nbp * 16, ls + row * nbp, nbp, g, lq, act[d]);
       wt[d] = !mine ? 0.0f : e < E ? w[p] : 1.0f;
     } else {
       const uint32_t row = (uint32_t)p * (uint32_t)nbp;
@@ -322,15 +358,15 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
 #pragma unroll
     for (int i = 0; i < RT; i++) {
       const uint32_t row = (uint32_t)(16 * i + li) * (uint32_t)nb;
-      if constexpr (AL16) {
-        const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ws, row + g * 16, 0, 0));
+      if constexpr (SL != SC_BYTES) {
+        const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ws, row + min(g * 16, nb - 16), 0, 0));
         wg[d][i].u[0] = u.x, wg[d][i].u[1] = u.y, wg[d][i].u[2] = u.z, wg[d][i].u[3] = u.w;
       }
 #pragma unroll
       for (int s = 0; s < 4; s++) {
-        const int b = AL16 ? g * 16 + 4 * s + lq : min(g * 16 + 4 * s + lq, nb - 1);  // past K: activations of zero
+        const int b = min(g * 16 + 4 * s + lq, nb - 1);  // past K: activations of zero
         wg[d][i].c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wc, (row + b) * 16, 0, 0));
-        if constexpr (!AL16) wg[d][i].u[s] = __builtin_amdgcn_raw_buffer_load_b8(ws, row + b, 0, 0);
+        if constexpr (SL == SC_BYTES) wg[d][i].u[s] = __builtin_amdgcn_raw_buffer_load_b8(ws, row + b, 0, 0);
       }
     }
     held[d] = li < T_ ? (e < E ? slots[e * DN_TOK + li] : 1u) : 0u;
@@ -345,13 +381,15 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
       const int u = u0 + DN_WAVES * d;
       if (u < units) {
         uint32_t mine = held[d];
+#pragma unroll
+        for (int i = 0; i < RT; i++) end_group<SL>(wg[d][i], nb, u % ng);
         while (true) {
 #pragma unroll
           for (int i = 0; i < RT; i++) {
             v4f dsum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < 4; s++)  // rows of the result: weight rows; columns: tokens
-              dsum = mx_mfma16(wg[d][i].c[s], group_scale<AL16>(wg[d][i], s, lq), act[d].c[s], group_scale<true>(act[d], s, lq), dsum);
+              dsum = mx_mfma16(wg[d][i].c[s], group_scale<SL>(wg[d][i], s, lq), act[d].c[s], group_scale<SC_FULL>(act[d], s, lq), dsum);
 #pragma unroll
             for (int r = 0; r < 4; r++) acc[i][r] = mine ? __builtin_fmaf(wt[d], dsum[r], acc[i][r]) : acc[i][r];
           }
@@ -414,18 +452,23 @@ bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && down_lds(a, true) <= 4
 // One row quantised by every workgroup
 bool mx_gemv_from_x(const MxArgs &a) { return a.M == 1 && mx_padded(a.K) / 32 * 17 <= 48 * 1024; }
 
-static bool scales_al16(const MxArgs &a) {
-  return (a.K / 32) % 16 == 0 && (uintptr_t)a.ws % 16 == 0 && a.ws_stride % 16 == 0;
+static ScaleLoad scale_load(const MxArgs &a) {
+  if (a.K < 512) return SC_BYTES;
+  return (a.K / 32) % 16 == 0 && (uintptr_t)a.ws % 16 == 0 && a.ws_stride % 16 == 0 ? SC_FULL : SC_ANY;
 }
 
 template <MxMode MODE, typename T, int NT, MxAct ACT>
 static hipError_t launch_gemv_al(const MxArgs &a, int ny, size_t lds, hipStream_t s) {
-  const dim3 g((unsigned)((a.N + 15) / 16), (unsigned)ny), b(256);
-  const bool al16 = scales_al16(a);
-  if (al16)
-    hipLaunchKernelGGL((mx_gemv_kernel<MODE, T, NT, ACT, true>), g, b, lds, s, a);
-  else
-    hipLaunchKernelGGL((mx_gemv_kernel<MODE, T, NT, ACT, false>), g, b, lds, s, a);
+  auto go = [&]<ScaleLoad SL>() {
+    constexpr int rows = gate_up_halves<MODE, ACT, SL>() ? 8 : 16;  // output columns of a workgroup
+    const dim3 g((unsigned)((a.N + rows - 1) / rows), (unsigned)ny), b(256);
+    hipLaunchKernelGGL((mx_gemv_kernel<MODE, T, NT, ACT, SL>), g, b, lds, s, a);
+  };
+  switch (scale_load(a)) {
+    case SC_FULL: go.template operator()<SC_FULL>(); break;
+    case SC_ANY: go.template operator()<SC_ANY>(); break;
+    default: go.template operator()<SC_BYTES>();
+  }
   return hipGetLastError();
 }
 
@@ -461,21 +504,23 @@ static hipError_t launch_down_t(const MxArgs &a, const int32_t *idx, const float
   const dim3 g((unsigned)((a.N + step - 1) / step), (unsigned)((a.M + DN_TOK - 1) / DN_TOK)), b(64 * DN_WAVES);
   const size_t lds = down_lds(a, a.x != nullptr);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, lds, s, a, step, idx, w, (T *)out); };
-  auto pick = [&]<MxAct ACT, bool AL16>() {
+  auto pick = [&]<MxAct ACT, ScaleLoad SL>() {
     if (step <= 16)
-      go(mx_down_kernel<T, ACT, AL16, 1>);
+      go(mx_down_kernel<T, ACT, SL, 1>);
     else
-      go(mx_down_kernel<T, ACT, AL16, 2>);
+      go(mx_down_kernel<T, ACT, SL, 2>);
   };
-  const bool al16 = scales_al16(a);
-  if (a.x && al16)
-    pick.template operator()<ACT_X, true>();
-  else if (a.x)
-    pick.template operator()<ACT_X, false>();
-  else if (al16)
-    pick.template operator()<ACT_WS, true>();
-  else
-    pick.template operator()<ACT_WS, false>();
+  auto with_x = [&]<ScaleLoad SL>() {
+    if (a.x)
+      pick.template operator()<ACT_X, SL>();
+    else
+      pick.template operator()<ACT_WS, SL>();
+  };
+  switch (scale_load(a)) {
+    case SC_FULL: with_x.template operator()<SC_FULL>(); break;
+    case SC_ANY: with_x.template operator()<SC_ANY>(); break;
+    default: with_x.template operator()<SC_BYTES>();
+  }
   return hipGetLastError();
 }
 

@@ -9,11 +9,13 @@
 // renorm (0 where that sum is 0), times scale. Slots that no expert is left for hold -1 and 0.
 //
 // One wavefront per token, bound by its instructions (a token's logits are 1 KB at most).
-// route_fast keeps the whole selection in fp32, a value to a register: one maximum over the
+// The kernel keeps the whole selection in fp32, a value to a register: one maximum over the
 // wavefront (six instructions) per slot. Logits are fp32 numbers, so without a bias it is exact;
 // with one (and for sums of two scores) its keys are within a known distance of the fp64 ones,
 // and where two keys whose order counts lie closer than that, the token goes through route_exact,
 // the same selection in fp64. Only the taken experts' scores are computed in fp64 otherwise.
+// 8191 tokens of 256 experts in 8 groups, 8 taken, with a bias: 15 us (20 with the selection in
+// fp64); 4093 of 64 experts, and one token, 6 us: the call. The 8.4 MB of logits alone need 2.
 #include "mxfp4_impl.h"
 
 namespace coli {

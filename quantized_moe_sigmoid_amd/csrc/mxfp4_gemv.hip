@@ -33,7 +33,7 @@ struct Group {
 // How a row's scales come in: SC_FULL: nb is a multiple of 16 and the scales are 16-byte aligned;
 // SC_ANY: 16 bytes at any address, nb >= 16 (a group that the row ends in takes the row's last 16,
 // shifted at the product); SC_BYTES: byte by byte, for shorter rows. 16 tokens of 64 experts,
-// K = 1920: gate/up 95 us with byte loads.
+// K = 1920: gate/up 94 us with byte loads, 47 with these.
 enum ScaleLoad { SC_FULL, SC_ANY, SC_BYTES };
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
@@ -120,8 +120,8 @@ enum MxAct { ACT_WS, ACT_X };  // activations: quantised in the workspace; one r
 
 // Gate and up rows of a product of one token (and of rows without whole aligned groups, whose
 // loads need more registers) share a tile of the matrix instruction, eight of each, which takes
-// half the registers; else a workgroup has 16 of each: over 16 tokens 244 us against 265, over
-// one 25.2 and 25.0.
+// half the registers; else a workgroup has 16 of each: of 16 tokens 243 us
+// against 265, of one 26 and 24.7.
 template <MxMode MODE, MxAct ACT, ScaleLoad SL>
 constexpr bool gate_up_halves() {
   return MODE == MX_GATEUP && (ACT == ACT_X || SL != SC_FULL);
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
   static_assert(ACT == ACT_WS || (NT == 1 && MODE != MX_DOWN));
   extern __shared__ __align__(16) uint8_t lds[];  // ACT_X: the quantised row
   __shared__ float red[4][NMAT][NT][16][17];
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int li = lane & 15, lq = lane >> 4;
   const int n0 = blockIdx.x * (HALVES ? 8 : 16);
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32;

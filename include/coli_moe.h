@@ -253,13 +253,13 @@ typedef struct {
  * [T][k] = the k best keys of the kept groups in descending order, every tie to the lower
  * index; topk_w fp32 [T][k] = p, with renorm over the sum of the taken (0 where that is 0),
  * times scale. Slots that no expert is left for hold -1 and 0, which coli_moe_group takes.
- * Follows colibri-strix README, "What's implemented", router item. */
+ * T < 2^26 - 3. Follows colibri-strix README, "What's implemented", router item. */
 int coli_moe_route_logits(const coli_moe_router *r, const void *z, int dtype, int32_t T, const float *bias,
                           int32_t *topk_idx, float *topk_w, void *stream);
 
 /* MXFP4 of rows x cols values (cols % 32 == 0; x and codes 16-byte aligned): codes
  * [rows][cols/2], scales [rows][cols/32]; and back, value = e2m1(code) * 2^(u - 127) rounded
- * to dtype (NaN for u = 255; out 16-byte aligned). */
+ * to dtype (NaN for u = 255; out 16-byte aligned). rows * cols / 32 <= 2^31 - 128. */
 int coli_moe_mxfp4_quantize(const void *x, int dtype, int64_t rows, int32_t cols, uint8_t *codes, uint8_t *scales,
                             void *stream);
 int coli_moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t cols, void *out,
@@ -268,7 +268,8 @@ int coli_moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64
 /* y [M][N] = MXFP4(x [M][K]) W^T, W's N rows given as codes [N][K/2] (16-byte aligned) and
  * scales [N][K/32] (any alignment). K % 32 == 0, x and y 16-byte aligned, y of x's dtype.
  * workspace: coli_moe_mxfp4_linear_workspace_bytes(M_max, N, K), 256-byte aligned, for every
- * M <= M_max (0 if a size is invalid; M = 0 or N = 0: a no-op). */
+ * M <= M_max (0 if a size is invalid; M = 0 or N = 0: a no-op). M, N, K <= 2^20; with K rounded up
+ * to 512, M * K < 2^36 - 4096 and N * K < 2^38 - 16384. */
 size_t coli_moe_mxfp4_linear_workspace_bytes(int32_t M_max, int32_t N, int32_t K);
 int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const uint8_t *scales, int32_t M, int32_t N,
                           int32_t K, void *y, void *workspace, size_t ws_bytes, void *stream);

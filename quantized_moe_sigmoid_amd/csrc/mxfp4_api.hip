@@ -108,6 +108,7 @@ int coli_moe_route_logits(const coli_moe_router *r, const void *z, int dtype, in
   if (r->score != COLI_SCORE_SIGMOID && r->score != COLI_SCORE_SOFTMAX) return COLI_E_INVALID;
   if (!(r->scale == r->scale)) return COLI_E_INVALID;  // NaN
   if (r->n_experts > 1024 || r->n_group > 64 || r->top_k > 64) return COLI_E_UNSUPPORTED;
+  if (T > (1 << 26) - 4) return COLI_E_UNSUPPORTED;  // 64 threads a token, fewer than 2^32
   if (T == 0) return COLI_OK;
   if (!z || !topk_idx || !topk_w) return COLI_E_INVALID;
   if (!mx_aligned(z, dtype == COLI_F32 ? 4 : 2) || !mx_aligned(topk_idx, 4) || !mx_aligned(topk_w, 4) ||

@@ -118,10 +118,10 @@ __device__ __forceinline__ void quantise_x(const T *x, int nb, int nbp, int tid,
 
 enum MxAct { ACT_WS, ACT_X };  // activations: quantised in the workspace; one row of x
 
-// Gate and up rows of a product of one token (and of rows without whole aligned groups, whose
-// loads need more registers) share a tile of the matrix instruction, eight of each, which takes
-// half the registers; else a workgroup has 16 of each: of 16 tokens 243 us
-// against 265, of one 26 and 24.7.
+// Do eight gate rows and the eight up rows of the same features share a tile of the matrix
+// instruction? It takes half the registers of 16 rows of each: one token 26 -> 24.7 us, and rows
+// that are no multiple of 16 blocks, whose loads need more registers, 94 -> 52 us (16 tokens,
+// K = 1920). Else activations are read twice as often: 16 tokens 243 -> 265 us.
 template <MxMode MODE, MxAct ACT, ScaleLoad SL>
 constexpr bool gate_up_halves() {
   return MODE == MX_GATEUP && (ACT == ACT_X || SL != SC_FULL);

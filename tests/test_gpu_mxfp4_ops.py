@@ -556,3 +556,22 @@ def test_down_token_blocks_bitidentical(q):
     perm, off, act, na = mxref.group(idx[16:], E)
     q.mxfp4_down(cfg, weights, rows, _t(idx[16:]), _t(w[16:]), *[_t(a) for a in (off, perm, act, na)], one, ws)
     assert torch.equal(out[16:], one)
+
+
+def test_gate_up_extremes_tiled(q):
+    """The same through the tiled kernel."""
+    test_gate_up_extremes(q, 300)
+
+
+@pytest.mark.parametrize("T,K", [(1, 1920), (1, 640), (5, 1152), (16, 896), (300, 1920)])
+def test_experts_rows_between_groups(q, T, K):
+    """Rows that end at every place of a group of 16 blocks that their length allows."""
+    for dtype in DT:
+        test_gate_up(q, (T, K, 256, 16, 2, True, 0, False), dtype)
+        test_down(q, (T, 256, K, 16, 2, True, 0, False), dtype)
+
+
+@pytest.mark.parametrize("blocks", range(16, 33))
+def test_linear_rows_between_groups(q, blocks):
+    _check_linear(q, 1, 40, 32 * blocks, "bfloat16", blocks)
+    _check_linear(q, 9, 40, 32 * blocks, "bfloat16", blocks)

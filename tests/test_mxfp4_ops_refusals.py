@@ -155,3 +155,5 @@ def test_sizes_beyond_one_launch(q):
     assert L.coli_moe_mxfp4_linear_workspace_bytes(16, 1 << 20, 1 << 20) == 0
     assert L.coli_moe_mxfp4_linear(P, 0, P, P, 1 << 20, 16, 1 << 20, P, P, 1 << 62, None) == -2
     assert L.coli_moe_mxfp4_linear_workspace_bytes(1 << 20, 16, 1 << 15) > 0
+    r = C.byref(q.make_router(8, 2))
+    assert L.coli_moe_route_logits(r, P, 0, (1 << 26) - 3, None, P, P, None) == -2

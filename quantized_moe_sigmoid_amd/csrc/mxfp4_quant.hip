@@ -53,27 +53,32 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(const uint8_t *__res
   *reinterpret_cast<v8 *>(out + blk * 32 + 16 + 8 * q) = hi;
 }
 
-// The activations of a product: rows of nb blocks, padded to nbp (zero codes, scale 1).
+// The activations of a product: rows of nb blocks, padded to nbp (zero codes, scale 1); fewer than
+// 2^31 blocks. Whole rows (nb == nbp) need no place in their row.
 template <typename T>
-__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(const T *__restrict__ x, int64_t rows, int nb, int nbp,
-                                                               uint8_t *__restrict__ codes,
+__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(const T *__restrict__ x, uint32_t blocks, uint32_t nb,
+                                                               uint32_t nbp, uint8_t *__restrict__ codes,
                                                                uint8_t *__restrict__ scales) {
-  const int64_t gid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t blk = gid >> 1;
+  const uint32_t blk = blockIdx.x * 128 + (threadIdx.x >> 1);
   const int q = threadIdx.x & 1;
-  const int64_t row = blk / nbp;
-  const int b0 = (int)(blk - row * nbp);
-  if (row >= rows) return;
+  if (blk >= blocks) return;  // both lanes of a block or neither
+  int64_t from = blk;
+  bool there = true;
+  if (nb != nbp) {
+    const uint32_t row = blk / nbp, b0 = blk - row * nbp;
+    there = b0 < nb;
+    from = (int64_t)row * nb + b0;
+  }
   uint2 w = make_uint2(0, 0);
   uint32_t u = 127;
-  if (b0 < nb) {
+  if (there) {
     float a[8], b[8];
-    const T *px = x + (row * nb + b0) * 32;
+    const T *px = x + from * 32;
     load8(px + 8 * q, a);
     load8(px + 16 + 8 * q, b);
     w = mx_quant_half(a, b, u);
   }
-  *reinterpret_cast<uint2 *>(codes + blk * 16 + 8 * q) = w;
+  *reinterpret_cast<uint2 *>(codes + (int64_t)blk * 16 + 8 * q) = w;
   if (q == 0) scales[blk] = (uint8_t)u;
 }
 
@@ -116,14 +121,14 @@ hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int
 
 hipError_t launch_mx_quantize_rows(const void *x, int dtype, int64_t rows, int K, uint8_t *codes, uint8_t *scales,
                                    hipStream_t s) {
-  const int nb = K / 32, nbp = mx_padded(K) / 32;
+  const uint32_t nb = K / 32, nbp = mx_padded(K) / 32, n = (uint32_t)(rows * nbp);
   const dim3 g(grid_of(rows * nbp)), b(256);
   if (dtype == COLI_F32)
-    hipLaunchKernelGGL(mx_quantize_rows_kernel<float>, g, b, 0, s, (const float *)x, rows, nb, nbp, codes, scales);
+    hipLaunchKernelGGL(mx_quantize_rows_kernel<float>, g, b, 0, s, (const float *)x, n, nb, nbp, codes, scales);
   else if (dtype == COLI_BF16)
-    hipLaunchKernelGGL(mx_quantize_rows_kernel<bf16_t>, g, b, 0, s, (const bf16_t *)x, rows, nb, nbp, codes, scales);
+    hipLaunchKernelGGL(mx_quantize_rows_kernel<bf16_t>, g, b, 0, s, (const bf16_t *)x, n, nb, nbp, codes, scales);
   else
-    hipLaunchKernelGGL(mx_quantize_rows_kernel<f16_t>, g, b, 0, s, (const f16_t *)x, rows, nb, nbp, codes, scales);
+    hipLaunchKernelGGL(mx_quantize_rows_kernel<f16_t>, g, b, 0, s, (const f16_t *)x, n, nb, nbp, codes, scales);
   return hipGetLastError();
 }
 

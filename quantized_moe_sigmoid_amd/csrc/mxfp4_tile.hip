@@ -13,12 +13,12 @@
 // full rate, close to what whole 128-byte lines reach (36; 64-byte pieces 22), hence stages of
 // 256 inputs, one row of a stage to a line. A wavefront's 128 x 128 part fills the accumulators.
 //
-// Over a route, 2048 tokens, 256 experts of 6144 x 2048, Zipf-like: gate/up 824 us, down 500 (and
+// Over a route, 2048 tokens, 256 experts of 6144 x 2048, Zipf-like: gate/up 811 us, down 480 (and
 // 96 for the combine). Bound by the weights' way from HBM: 3.4 GB, of which the kernel fetches
-// 3.9 (a line of scale bytes comes back for every two stages). Without products 804 us, without
-// scales 749. Three buffers (960 us with two); 8 wavefronts to the tile 851, two workgroups of
-// 128 x 128 tiles to a CU 857; column strips of 1, 2, 3 and 4 tiles 822, 824, 855 and 869 us for
-// gate/up, 613, 598, 599 and 599 for down.
+// 3.9 (a line of scale bytes comes back for every two stages). Measured when the whole took 825:
+// without products 804, without scales 749; 8 wavefronts to the tile 851 (with two stages in LDS
+// instead of three 960), two workgroups of 128 x 128 tiles to a CU 857; column strips of 1, 2, 3
+// and 4 tiles 822, 825, 855 and 869 us for gate/up, 613, 598, 599 and 599 for down.
 #include <type_traits>
 
 #include "mxfp4_impl.h"
@@ -248,6 +248,12 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     };
     constexpr int ISSUES = QA + QB + S::LS, LOADS = NA + S::LB + S::LS;
     static_assert((NBUF - 1) * LOADS <= 63, "vmcnt");
+    // The first EARLY issues of a stage go out in the K step after the barrier, the others in the
+    // next one. With three buffers there is time: a quarter early 811 us for gate/up of 2048
+    // tokens, half 816, all 825; with two (dense) half: the same as all, a quarter 2 % slower.
+    constexpr int EARLY = NBUF > 2 ? ISSUES / 4 : ISSUES / 2;
+    constexpr int EARLY_LOADS = EARLY <= QA ? (EARLY * 2 < NA ? EARLY * 2 : NA)
+                              : EARLY <= QA + QB ? NA + (EARLY - QA) * 2 : NA + S::LB + (EARLY - QA - QB);
     auto issue_end = [&]() {
       slot = slot == NBUF - 1 ? 0 : slot + 1;
       left--;
@@ -309,17 +315,17 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     };
 
     // While a stage is multiplied the NBUF - 1 after it are on their way. Its last K step is in
-    // registers before its buffer is given up, and is multiplied while the loads of stage + NBUF
-    // and the first fragments of the next stage are under way. The products' part of the body
+    // registers before its buffer is given up, and is multiplied while the first loads of stage
+    // + NBUF and the first fragments of the next stage are under way. The products' part of the body
     // has no branch: the compiler would move products across it, behind the wait.
 #pragma unroll
     for (int s = 0; s < NBUF; s++) {
       issue_start();
 #pragma unroll
-      for (int q = 0; q < ISSUES; q++) issue(q);
-      issue_end();
+      for (int q = 0; q < (s < NBUF - 1 ? ISSUES : EARLY); q++) issue(q);
+      if (s < NBUF - 1) issue_end();
     }
-    wait_loads<(NBUF - 1) * LOADS>();
+    wait_loads<(NBUF - 2) * LOADS + EARLY_LOADS>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     int cur = 0, cwin = 0;  // buffer slot and window of the stage that is multiplied
@@ -343,6 +349,12 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
             mul(t, q / NI, q % NI);
 #pragma unroll
             for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(cur, t + 1, p);
+            if (t == 0) {
+              constexpr int PER0 = (ISSUES - EARLY + MUL - 1) / MUL;
+#pragma unroll
+              for (int p = EARLY + q * PER0; p < EARLY + (q + 1) * PER0 && p < ISSUES; p++) issue(p);
+              if (q == MUL - 1) issue_end();
+            }
             __builtin_amdgcn_sched_barrier(0);
           }
         const bool last = s == nst - 1;
@@ -353,19 +365,18 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        constexpr int PER = (ISSUES + MUL - 1) / MUL;
+        constexpr int PER = (EARLY + MUL - 1) / MUL;
 #pragma unroll
         for (int q = 0; q < MUL; q++) {
           __builtin_amdgcn_sched_barrier(0);
           mul(KS - 1, q / NI, q % NI);
           if (q == 0) read_scales(next, cwin, ns);  // past the last stage: not used
 #pragma unroll
-          for (int p = q * PER; p < (q + 1) * PER && p < ISSUES; p++) issue(p);
+          for (int p = q * PER; p < (q + 1) * PER && p < EARLY; p++) issue(p);
 #pragma unroll
           for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(next, 0, p);
         }
         __builtin_amdgcn_sched_barrier(0);
-        issue_end();
         take_scales();
         cur = next;
       }

@@ -9,7 +9,7 @@
 // activations (x in ACT_X) is quantised by every workgroup itself while its first weights are
 // under way, which saves a launch. One token, bf16: dense 12288 x 6144 8.3 to 9 us (40 MB, 6.4 us
 // at the 6.3 TB/s of a plain streaming read, and a launch), gate/up of 9 experts of 6144 x 2048
-// 24.5 us (120 MB, 4.9 TB/s); gate/up of 16 tokens over 256 experts 243 us (5.7 TB/s).
+// 23 to 24.5 us (120 MB, 5 TB/s); gate/up of 16 tokens over 256 experts 243 us (5.7 TB/s).
 //
 // mx_down_kernel: the down product of few tokens (16 to a workgroup) with its weighted combine. A
 // workgroup (8 wavefronts) owns 8 to 32 output rows of its tokens and goes through all experts

@@ -4,7 +4,9 @@
 // of OCP MX v1.0, in mx_quant_half (mxfp4_impl.h).
 //
 // Bound by memory: a value is read once and 17/32 byte of it written (and the reverse). Two
-// lanes own a block, so every load is 16 bytes wide and every store of codes 8 bytes.
+// lanes own a block, so every load is 16 bytes wide and every store of codes 8 bytes. 49152 x 2048
+// bf16: 58 us to codes (254 MB, 4.4 TB/s), 39 us back (6.5 TB/s), copies reaching 4.7 to 4.9;
+// two or four blocks to a thread: 2 to 5 us slower.
 #include "mxfp4_impl.h"
 
 namespace coli {

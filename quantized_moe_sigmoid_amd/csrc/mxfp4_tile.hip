@@ -5,7 +5,7 @@
 // y = sum over blocks of 2^(ua - 127) 2^(uw - 127) sum a_i w_i: the instruction takes both
 // operands' codes and their E8M0 bytes, so a block costs no work of the vector units.
 //
-// Dense, M = 4096, N = 12288, K = 6144 bf16: 180 to 195 us (3.2 to 3.4 PFLOP/s). The instruction
+// Dense, M = 4096, N = 12288, K = 6144 bf16: 177 to 195 us (3.2 to 3.5 PFLOP/s). The instruction
 // on random codes in registers alone reaches 6.1 to 6.4 PFLOP/s here (9.2 on zeros: the card's
 // power, not the issue rate, is the limit), which is 100 us; without its products the kernel
 // takes 145, without scales too 132: the tile's way through L2 and LDS and the matrix cores each

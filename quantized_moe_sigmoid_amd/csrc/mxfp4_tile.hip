@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "mxfp4_impl.h"
+#include "mxfp4_tile_plan.h"
 
 namespace coli {
 
@@ -123,32 +124,31 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / S::WN, wn = wv % S::WN;
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, nst = (nb + KB - 1) / KB;
-  const int nx = (a.N + BF - 1) / BF;
+  const int ns = tile_strips(a.N, BF, a.strip);
 
   // the rows of activations: first .. first + n - 1 of perm, or of the tokens; and the column
   // tiles bx .. bx + cols - 1, one after another
   int bx, by, cols, e = 0, first = 0, n = 0;
   bool routed = false;
   if constexpr (MODE == MX_LINEAR) {
-    tile_of(blockIdx.x, (nx + a.strip - 1) / a.strip, (a.M + BM - 1) / BM, bx, by);
-    bx *= a.strip;
-    cols = min(a.strip, nx - bx);
+    int sx;
+    tile_of(blockIdx.x, ns, (a.M + BM - 1) / BM, sx, by);
+    strip_tiles(a.N, BF, a.strip, sx, bx, cols);
     first = by * BM;
     n = min(BM, a.M - first);
   } else {
     // Each XCD (id % 8) gets a run of (group of an expert's row tiles, column strip, row tile),
     // the row tile fastest: the workgroups that read the same weights run next to each other on
     // one XCD and share them in its L2; the strips of a group share its activations there.
-    const int nt = *a.ntiles, ns = (nx + a.strip - 1) / a.strip, xcd = blockIdx.x & 7, total = nt * ns;
+    const int nt = *a.ntiles, xcd = blockIdx.x & 7, total = nt * ns;
     const int q = total >> 3, r = total & 7, local = blockIdx.x >> 3;
     if (local >= q + (xcd < r)) return;
     const int t = xcd * q + min(xcd, r) + local;
     by = t / ns;
     int4 c = a.tiles[by];
     const int grp = c.w >> 16, b0 = by - ((c.w >> 8) & 0xFF), in = t - b0 * ns;
-    bx = in / grp * a.strip;
+    strip_tiles(a.N, BF, a.strip, in / grp, bx, cols);
     by = min(b0 + in % grp, nt - 1);
-    cols = min(a.strip, nx - bx);
     c = a.tiles[by];
     e = c.x;
     first = c.y;
@@ -176,9 +176,7 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     return MODE == MX_DOWN ? ids[i] : (routed ? ids[i] / a.k : ids[i] - (int)P);
   };
   auto w_row = [&](int r) -> int {  // weight row of column r of the first tile, relative to the base below
-    if constexpr (MODE == MX_GATEUP)  // by eights: gate rows, then the up rows of the same features
-      return (r >> 3 & 1) * a.N + min((r >> 4) * 8 + (r & 7), a.N - 1 - bx * BF);
-    return min(r, a.N - 1 - bx * BF);
+    return tile_weight_row(MODE == MX_GATEUP, r, a.N, bx * BF);
   };
   // tile-relative bases keep the lanes' offsets within 32 bits
   const uint8_t *ac = a.ac, *as = a.as;
@@ -458,7 +456,6 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
 // Row tiles of an expert that go through a column strip together, so that its weights come from
 // the fabric once (4.23 -> 3.95 GB for gate/up of 2048 tokens); 2 and 8: 833 and 825 us
 constexpr int EXP_GROUP = 8;
-constexpr int EXP_STRIP = 2;  // column tiles of a workgroup
 
 // Tile c of an expert's `all`: its w entry, routed | place in its group << 8 | size of the group << 16
 __device__ __forceinline__ int tile_place(int c, int all, int routed) {
@@ -500,20 +497,6 @@ __global__ __launch_bounds__(1024) void mx_plan_kernel(MxArgs a, int bm, int cap
   if (tid == 0) *a.ntiles = min(total, cap);
 }
 
-// Column tiles of a dense workgroup: `slots` workgroups run at a time, and a strip's start and
-// end cost about a third of a tile.
-constexpr int MX_CUS = 256;
-static int dense_strip(int nx, int ny, int slots) {
-  int best = 1;
-  double cost = 1e300;
-  for (int s = 1; s <= 8 && s <= nx; s++) {
-    const int64_t groups = (int64_t)((nx + s - 1) / s) * ny;
-    const double c = (double)((groups + slots - 1) / slots) * (s + 0.33);
-    if (c < cost) cost = c, best = s;
-  }
-  return best;
-}
-
 template <MxMode MODE, typename T, typename S, bool RAGGED = false>
 static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static_assert(S::BYTES <= 160 * 1024, "LDS");
@@ -522,10 +505,8 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (attr != hipSuccess) return attr;
-  const int nx = (a.N + BF - 1) / BF;
-  a.strip = MODE == MX_LINEAR ? dense_strip(nx, ny, MX_CUS * S::OCC) : EXP_STRIP;
-  const unsigned gx = (unsigned)((nx + a.strip - 1) / a.strip);
-  const unsigned groups = gx * (unsigned)ny;
+  a.strip = MODE == MX_LINEAR ? dense_strip(a.N, BF, ny, MX_CUS * S::OCC) : EXP_STRIP;
+  const unsigned groups = (unsigned)tile_strips(a.N, BF, a.strip) * (unsigned)ny;
   hipLaunchKernelGGL(kernel, dim3(MODE == MX_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);
   return hipGetLastError();
 }

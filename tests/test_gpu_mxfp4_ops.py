@@ -575,3 +575,15 @@ def test_experts_rows_between_groups(q, T, K):
 def test_linear_rows_between_groups(q, blocks):
     _check_linear(q, 1, 40, 32 * blocks, "bfloat16", blocks)
     _check_linear(q, 9, 40, 32 * blocks, "bfloat16", blocks)
+
+
+# a short last column tile behind strips of several whole ones: 128 x 128 tiles, 256 x 256 tiles
+@pytest.mark.parametrize("M,N,K", [(1000, 11003, 96), (2048, 9000, 96), (1800, 9001, 544)])
+def test_linear_short_tile_after_strips(q, M, N, K):
+    print(f"linear M={M} N={N} K={K}", flush=True)
+    _check_linear(q, M, N, K, "bfloat16", M + N + K)
+
+
+@pytest.mark.parametrize("H", [384, 896, 1408, 1920])
+def test_down_short_tile_after_strips(q, H):
+    test_down(q, (300, H, 256, 16, 2, True, 0, False), "bfloat16")

@@ -56,28 +56,6 @@ __device__ __forceinline__ void wait_loads() {  // all but the last N loads of t
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// BM x BN tile, WM x WN wavefronts, NBUF K stages of 8 blocks (256 inputs) in LDS, OCC workgroups per CU
-template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int OCC_, bool WIDE_ = true>
-struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_, OCC = OCC_;
-  static constexpr int KB = 8, KS = 4;                          // blocks of a stage, its K steps of 64 inputs
-  static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;    // 32 x 32 tiles of a wavefront
-  static constexpr int ROWS = BM + BN;
-  static constexpr int LA = BM / 32, LB = BN / 32;              // 16-byte loads of a wavefront per stage (8 rows each)
-  // Scales. WIDE: a window of 16 bytes of a row serves two stages (rows of 16 blocks or more);
-  // it is loaded with the first (with the second its loads are empty) and NSB windows are held.
-  // Else: the two dwords of a stage with the stage.
-  static constexpr bool WIDE = WIDE_;
-  static constexpr int NSB = 1 + NBUF / 2;
-  static constexpr int RA = BM / 4, RB = BN / 4;                // scale rows of a wavefront
-  static constexpr int LS = WIDE ? 2 : 4;
-  static constexpr int STAGE = ROWS * (KB * 16 + (WIDE ? 0 : 8));  // LDS bytes: codes, then two planes of dwords
-  static constexpr int WINDOWS = NBUF * STAGE;                     // offset of the windows
-  static constexpr int IDS = WINDOWS + (WIDE ? NSB * ROWS * 16 : 0);  // offset of the row ids
-  static constexpr int BYTES = IDS + BM * 4;
-  static_assert(LB % 2 == 0 && RA <= 64 && RB <= 64);
-};
-
 typedef uint32_t v2u32 __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u32 __attribute__((ext_vector_type(4)));
 
@@ -203,19 +181,21 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
   const int wlast = a.ws_pitch - 16;  // the last window ends with the row
 
   auto run = [&]<int MX>() {  // with MX 32-row tiles to a wavefront
-    // The loads run ahead of the products, over the stages of all column tiles: stage si of the
-    // tile whose weights start at pb, buffer slot, window counter.
-    int si = 0, slot = 0, win = 0, left = cols * nst;
+    // The loads run ahead of the products, over the stages of all column tiles, of the one whose
+    // weights start at pb.
+    TilePlace<S> ahead;
+    int left = cols * nst;
     const uint8_t *pb = wc, *psb = ws;
     int on = -1;            // 0 once every stage is under way: the loads are empty
     uint32_t past = 0;      // past_k at a row's last stage
     auto issue_start = [&]() {
       on = __builtin_amdgcn_readfirstlane(-left >> 31);
-      past = si == nst - 1 ? past_k : 0u;
+      past = ahead.stage == nst - 1 ? past_k : 0u;
     };
     constexpr int NA = S::WM == 1 ? MX : S::LA, QA = (NA + 1) / 2, QB = S::LB / 2;  // the codes' loads go in pairs; an odd one alone
     auto issue = [&](int q) {  // load or pair q of the stage
-      const uint32_t buf = lds0 + slot * S::STAGE;
+      const int si = ahead.stage;
+      const uint32_t buf = lds0 + ahead.slot * S::STAGE;
       if (q < QA) {
         const uint32_t dst = buf + (8 * q + wv) * 1024;
         if (2 * q + 1 < NA)
@@ -227,7 +207,7 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
         dma16_pair(pb + si * (KB * 16), ob[2 * i] - past, ob[2 * i + 1] - past,
                    buf + BM * (KB * 16) + (8 * i + wv) * 1024, on, on);
       } else if constexpr (S::WIDE) {
-        const uint32_t dst = lds0 + S::WINDOWS + win * (S::ROWS * 16);
+        const uint32_t dst = lds0 + S::WINDOWS + ahead.win * (S::ROWS * 16);
         const int at = min(si * KB, wlast);
         const int fresh = on & ((si & 1) - 1);  // the first of the window's two stages
         if (q == QA + QB)
@@ -250,16 +230,12 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     // next one. With three buffers there is time: a quarter early 811 us for gate/up of 2048
     // tokens, half 816, all 825; with two (dense) half: the same as all, a quarter 2 % slower.
     constexpr int EARLY = NBUF > 2 ? ISSUES / 4 : ISSUES / 2;
+    static_assert(EARLY <= QA + QB, "scale windows are filled one barrier later than codes");
     constexpr int EARLY_LOADS = EARLY <= QA ? (EARLY * 2 < NA ? EARLY * 2 : NA)
                               : EARLY <= QA + QB ? NA + (EARLY - QA) * 2 : NA + S::LB + (EARLY - QA - QB);
     auto issue_end = [&]() {
-      slot = slot == NBUF - 1 ? 0 : slot + 1;
       left--;
-      si++;
-      const bool wrap = si == nst;
-      if ((si & 1) == 0 || wrap) win = win == S::NSB - 1 ? 0 : win + 1;
-      if (wrap) {
-        si = 0;
+      if (ahead.advance(nst)) {
         pb += (int64_t)BF * nb * 16;
         psb += (int64_t)BF * a.ws_pitch;
       }
@@ -326,7 +302,7 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
     wait_loads<(NBUF - 2) * LOADS + EARLY_LOADS>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    int cur = 0, cwin = 0;  // buffer slot and window of the stage that is multiplied
+    TilePlace<S> at;  // the stage that is multiplied
     read_scales(0, 0, 0);
 #pragma unroll
     for (int p = 0; p < MX + NI; p++) read(0, 0, p);
@@ -346,7 +322,7 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
           for (int q = 0; q < MUL; q++) {
             mul(t, q / NI, q % NI);
 #pragma unroll
-            for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(cur, t + 1, p);
+            for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(at.slot, t + 1, p);
             if (t == 0) {
               constexpr int PER0 = (ISSUES - EARLY + MUL - 1) / MUL;
 #pragma unroll
@@ -355,9 +331,7 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
             }
             __builtin_amdgcn_sched_barrier(0);
           }
-        const bool last = s == nst - 1;
-        const int next = cur == NBUF - 1 ? 0 : cur + 1, ns = last ? 0 : s + 1;
-        if ((s & 1) || last) cwin = cwin == S::NSB - 1 ? 0 : cwin + 1;
+        at.advance(nst);
         issue_start();
         wait_loads<(NBUF - 2) * LOADS>();  // the next stage has arrived; this one is in registers
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -368,15 +342,14 @@ __global__ __launch_bounds__(256, S::OCC) void mx_tile_kernel(MxArgs a) {
         for (int q = 0; q < MUL; q++) {
           __builtin_amdgcn_sched_barrier(0);
           mul(KS - 1, q / NI, q % NI);
-          if (q == 0) read_scales(next, cwin, ns);  // past the last stage: not used
+          if (q == 0) read_scales(at.slot, at.win, at.stage);  // past the last stage: not used
 #pragma unroll
           for (int p = q * PER; p < (q + 1) * PER && p < EARLY; p++) issue(p);
 #pragma unroll
-          for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(next, 0, p);
+          for (int p = q * RP; p < (q + 1) * RP && p < MX + NI; p++) read(at.slot, 0, p);
         }
         __builtin_amdgcn_sched_barrier(0);
         take_scales();
-        cur = next;
       }
       // Results: lane column li (a row of activations) of a 32 x 32 tile, rows (weight rows)
       // 8 (r / 4) + 4 hh + r % 4, so that a lane holds runs of four output columns. Two bytes to a
@@ -505,19 +478,15 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (attr != hipSuccess) return attr;
-  a.strip = MODE == MX_LINEAR ? dense_strip(a.N, BF, ny, MX_CUS * S::OCC) : EXP_STRIP;
+  a.strip = MODE == MX_LINEAR ? dense_strip(a.N, BF, ny, MX_CUS * S::OCC) : expert_strip<S>(a.K / 32);
   const unsigned groups = (unsigned)tile_strips(a.N, BF, a.strip) * (unsigned)ny;
   hipLaunchKernelGGL(kernel, dim3(MODE == MX_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);
   return hipGetLastError();
 }
 
-typedef TileShape<256, 256, 2, 2, 2, 1> TileDense;
-typedef TileShape<128, 128, 1, 4, 2, 2> TileDenseSmall;
 // Fewer big tiles than this leave too many CUs without work. K = 6144, N = 12288: 26 us against 49
 // with 48 big tiles (M = 256), 61 against 57 with 192; K = 2048, N = 4096: 20 against 27 with 128.
 constexpr int DENSE_BIG_TILES = 192;
-typedef TileShape<128, 256, 1, 4, 3, 1> TileExperts;
-typedef TileShape<128, 256, 1, 4, 3, 1, false> TileExpertsShort;  // fewer than 16 blocks in a row
 
 int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared) {
   const int64_t P = (int64_t)T * k, bm = TileExperts::BM;

@@ -6,7 +6,59 @@
 namespace coli {
 
 constexpr int MX_CUS = 256;
-constexpr int EXP_STRIP = 2;  // column tiles of a workgroup over a route
+
+// BM x BN tile, WM x WN wavefronts, NBUF K stages of 8 blocks (256 inputs) in LDS, OCC workgroups per CU
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int OCC_, bool WIDE_ = true>
+struct TileShape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_, OCC = OCC_;
+  static constexpr int KB = 8, KS = 4;                          // blocks of a stage, its K steps of 64 inputs
+  static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;    // 32 x 32 tiles of a wavefront
+  static constexpr int ROWS = BM + BN;
+  static constexpr int LA = BM / 32, LB = BN / 32;              // 16-byte loads of a wavefront per stage (8 rows each)
+  // Scales. WIDE: a window of 16 bytes of a row serves two stages (rows of 16 blocks or more);
+  // it is loaded with the first (with the second its loads are empty) and NSB windows are held.
+  // Else: the two dwords of a stage with the stage.
+  static constexpr bool WIDE = WIDE_;
+  static constexpr int NSB = 1 + NBUF / 2;
+  static constexpr int RA = BM / 4, RB = BN / 4;                // scale rows of a wavefront
+  static constexpr int LS = WIDE ? 2 : 4;
+  static constexpr int STAGE = ROWS * (KB * 16 + (WIDE ? 0 : 8));  // LDS bytes: codes, then two planes of dwords
+  static constexpr int WINDOWS = NBUF * STAGE;                     // offset of the windows
+  static constexpr int IDS = WINDOWS + (WIDE ? NSB * ROWS * 16 : 0);  // offset of the row ids
+  static constexpr int BYTES = IDS + BM * 4;
+  static_assert(LB % 2 == 0 && RA <= 64 && RB <= 64);
+};
+
+typedef TileShape<256, 256, 2, 2, 2, 1> TileDense;
+typedef TileShape<128, 128, 1, 4, 2, 2> TileDenseSmall;
+typedef TileShape<128, 256, 1, 4, 3, 1> TileExperts;
+typedef TileShape<128, 256, 1, 4, 3, 1, false> TileExpertsShort;  // fewer than 16 blocks in a row
+
+// A place in the stages of a workgroup's column tiles, of nst stages each, one after another: the
+// loads' and, NBUF - 1 stages behind, the products'.
+template <typename S>
+struct TilePlace {
+  int stage = 0, slot = 0, win = 0;  // stage of the column tile, its buffer and (WIDE) scale window
+  __host__ __device__ bool advance(int nst) {  // true: on to the next column tile
+    slot = slot == S::NBUF - 1 ? 0 : slot + 1;
+    stage++;
+    const bool wrap = stage == nst;
+    if ((stage & 1) == 0 || wrap) win = win == S::NSB - 1 ? 0 : win + 1;
+    if (wrap) stage = 0;
+    return wrap;
+  }
+};
+
+// Column tiles of a workgroup over a route, rows of nb blocks: two, but one where an odd number of
+// stages with scale windows ends in a window of one stage. Three windows are live at the way to a
+// next column tile then, two are held (a third passes the LDS), and the first of the next tile would
+// be filled while other wavefronts still read the window it replaces. Strips of 1 and 2: gate/up of
+// 2048 tokens over 256 experts of 6144 x 2048 822 and 825 us, down 613 and 598.
+template <typename S>
+inline int expert_strip(int nb) {
+  const int nst = (nb + S::KB - 1) / S::KB;
+  return S::WIDE && (nst & 1) ? 1 : 2;
+}
 
 __host__ __device__ inline int tile_min(int a, int b) { return a < b ? a : b; }
 

@@ -6,7 +6,46 @@
 
 using namespace coli;
 
+// The buffers and scale windows of a workgroup's `cols` column tiles of nst stages. Barriers cut the
+// work into intervals; wavefronts differ by less than one. Interval 0 loads stages 0 .. NBUF - 2
+// and the codes' first part of stage NBUF - 1; interval n + 1 multiplies stage n: it reads its
+// codes and (at its start) its scales, loads the rest of stage n + NBUF - 1, its scales among it,
+// and before that, behind the barrier that ended stage n - 1, the first codes of the same stage.
+// 0 if no stage's data is overwritten in the interval that reads it or before, and the products'
+// place finds what the loads' place wrote; else the failing rule.
+template <typename S>
+static int walk_stages(int nst, int cols) {
+  const int total = nst * cols;
+  TilePlace<S> in[512];
+  if (total >= 512) return -1;
+  for (int m = 0; m + 1 < total; m++) {
+    in[m + 1] = in[m];
+    if (in[m + 1].advance(nst) != (in[m + 1].stage == 0)) return 1;
+  }
+  TilePlace<S> out;  // the products' place
+  for (int n = 0; n < total; n++) {
+    if (out.slot != in[n].slot || out.win != in[n].win || out.stage != in[n].stage) return 2;
+    const int w = n - (in[n].stage & 1);  // the stage whose loads brought its window
+    if (in[w].win != in[n].win) return 3;
+    for (int m = 0; m < total; m++) {
+      const int scales_in = m < S::NBUF - 1 ? 0 : m - S::NBUF + 2, codes_in = m < S::NBUF ? 0 : m - S::NBUF + 2;
+      if (m > n && in[m].slot == in[n].slot && codes_in <= n + 1) return 4;
+      if (!S::WIDE || (in[m].stage & 1) || in[m].win != in[n].win) continue;
+      if (m > w && scales_in <= n + 1) return 5;  // refilled while, or before, stage n's scales are read
+    }
+    out.advance(nst);
+  }
+  return 0;
+}
+
 extern "C" {
+
+int walk_dense(int nst, int cols) { return walk_stages<TileDense>(nst, cols); }
+int walk_dense_small(int nst, int cols) { return walk_stages<TileDenseSmall>(nst, cols); }
+int walk_experts(int nst, int cols) { return walk_stages<TileExperts>(nst, cols); }
+int walk_experts_short(int nst, int cols) { return walk_stages<TileExpertsShort>(nst, cols); }
+int strip_experts(int nb) { return expert_strip<TileExperts>(nb); }
+int strip_experts_short(int nb) { return expert_strip<TileExpertsShort>(nb); }
 
 int dense_strip_of(int N, int BF, int ny, int slots) { return dense_strip(N, BF, ny, slots); }
 

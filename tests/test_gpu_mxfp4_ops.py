@@ -587,3 +587,10 @@ def test_linear_short_tile_after_strips(q, M, N, K):
 @pytest.mark.parametrize("H", [384, 896, 1408, 1920])
 def test_down_short_tile_after_strips(q, H):
     test_down(q, (300, H, 256, 16, 2, True, 0, False), "bfloat16")
+
+
+@pytest.mark.parametrize("K", [640, 768, 1152, 1280, 1664, 2176])
+def test_experts_odd_stages_of_several_column_tiles(q, K):
+    """Rows of 3, 5, 7 and 9 stages of 256 inputs, several column tiles, tokens past one row tile."""
+    test_gate_up(q, (300, K, 512, 8, 2, True, 0, False), "bfloat16")
+    test_down(q, (300, 1024, K, 8, 2, True, 0, False), "bfloat16")

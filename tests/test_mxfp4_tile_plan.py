@@ -1,5 +1,6 @@
 """The plan of the tiled MXFP4 products, walked on the CPU from the header that the kernels use:
-every weight row a workgroup loads lies in the matrix (CPU only, no kernel runs)."""
+every weight row a workgroup loads lies in the matrix, and no buffer or scale window is filled
+again before every wavefront has read it (CPU only, no kernel runs)."""
 import ctypes as C
 import os
 import shutil
@@ -43,3 +44,29 @@ def test_expert_weight_rows_stay_inside(plan, strip):
     for n in range(128, 8192 + 128, 128):
         assert plan.walk_rows(0, n, 256, strip) >= 0, n
         assert plan.walk_rows(1, n, 256, strip) >= 0, n
+
+
+def test_expert_buffers_and_windows_are_read_before_they_are_refilled(plan):
+    """Rows of every multiple of 128 inputs that the experts' products take on the tiled kernel."""
+    for nb in range(4, 260, 4):
+        nst = (nb + 7) // 8
+        if nb >= 16:
+            for cols in range(1, plan.strip_experts(nb) + 1):
+                assert plan.walk_experts(nst, cols) == 0, (nb, cols)
+        else:
+            for cols in range(1, plan.strip_experts_short(nb) + 1):
+                assert plan.walk_experts_short(nst, cols) == 0, (nb, cols)
+
+
+def test_walk_sees_a_window_refilled_early(plan):
+    """Three buffers, an odd number of stages, two column tiles: the walk reports the conflict."""
+    for nst in range(3, 33, 2):
+        assert plan.walk_experts(nst, 2) == 5
+        assert plan.walk_experts(nst + 1, 2) == 0
+
+
+@pytest.mark.parametrize("cols", range(1, 9))
+def test_dense_buffers_and_windows_are_read_before_they_are_refilled(plan, cols):
+    for nst in range(1, 60):
+        assert plan.walk_dense(nst, cols) == 0, nst
+        assert plan.walk_dense_small(nst, cols) == 0, nst

@@ -302,9 +302,17 @@ __global__ __launch_bounds__(64 * RL_WAVES) void route_logits_kernel(RouteLogits
     }
     const bool keep = before < a.Gk;
     if (scores) {
-      const int in = ~wave_max(keep && g < G ? ~gs : ABSENT), out = wave_max(!keep && g < G ? gs : ABSENT);
-      const float fi = value_of(in), fo = value_of(out);
-      close = out != ABSENT && !(fi - fo > 4 * delta + (fabsf(fi) + fabsf(fo)) * 0x1p-21f);
+      // A group's one or two keys were rounded at their own sizes and may cancel in the sum: its
+      // error is below 2 delta + (|b1| + |b2|) 2^-22. Compared are the least that a kept group can
+      // be and the most that another can (infinite sizes: close).
+      const float f1 = value_of(b1), f2 = two && b2 != ABSENT ? value_of(b2) : 0.0f;
+      const float mag = fabsf(f1) + fabsf(f2), err = mag < INFINITY ? mag * 0x1p-21f : INFINITY, sum = value_of(gs);
+      const int least = err < INFINITY ? order_of(sum - err) : ABSENT;
+      const int most = order_of(err < INFINITY ? sum + err : INFINITY);
+      const bool there = g < G && gs != ABSENT;
+      const int in = ~wave_max(keep && g < G ? ~(there ? least : ABSENT) : ABSENT);
+      const int out = wave_max(!keep && there ? most : ABSENT);
+      close = out != ABSENT && !(value_of(in) - value_of(out) > 4 * delta);
     }
 #pragma unroll
     for (int i = 0; i < EPL; i++) ord[i] = keep ? ord[i] : ABSENT;

@@ -134,3 +134,31 @@ def test_route_empty_and_refused(q):
     with pytest.raises(q.ColiError) as e:
         q.route_logits(q.make_router(16, 4, 2, 3), z, i, w)
     assert e.value.status == q.COLI_E_INVALID
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("B", [1.0, 64.0, 512.0, 2.0 ** 14, 2.0 ** 22, 2.0 ** 40, 3e38])
+@pytest.mark.parametrize("E,m,Gk", [(8, 2, 1), (16, 2, 3), (64, 8, 4)])
+def test_route_groups_whose_best_cancel(q, E, m, Gk, B, score):
+    """Groups by their two best, whose biases are B and -B: the sum is small, what its two keys were
+    rounded by is not. Logits a little apart, so that groups differ by less than that."""
+    rng = np.random.default_rng(E + int(np.log2(B)))
+    T, G = 400, E // m
+    z = 0.5 * rng.standard_normal((T, 1)) + 4e-5 * rng.standard_normal((T, E))
+    bias = np.full(E, -np.inf)
+    bias[::m], bias[1::m] = B, -B
+    if m > 2:
+        bias[2::m] = -3e38  # present and never among the two best (but equal to them at the largest B)
+    _run(q, z, min(8, 2 * Gk), bias=bias, G=G, Gk=Gk, score=score, group_top=2, scale=2.5)
+
+
+def test_route_groups_one_of_which_cancels(q):
+    """One group's biases cancel, the others have none."""
+    rng = np.random.default_rng(12)
+    T, E, G = 500, 32, 8
+    for B in (64.0, 700.0, 1e5):
+        z = 0.3 * rng.standard_normal((T, 1)) + 4e-5 * rng.standard_normal((T, E))
+        bias = np.zeros(E)
+        bias[8], bias[9], bias[10], bias[11] = B, -B, -4 * B, -4 * B
+        _run(q, z, 6, bias=bias, G=G, Gk=3, group_top=2)
+        _run(q, z, 6, bias=bias, G=G, Gk=3, group_top=1)

@@ -6,8 +6,20 @@
 #pragma once
 
 #include "coli_internal.h"
+#include "per_device.h"
 
 namespace coli {
+
+// The current device lets `kernel` have `bytes` of LDS (64 KB without asking)
+template <typename Kernel>
+inline hipError_t allow_lds(PerDevice &done, Kernel kernel, size_t bytes) {
+  int device = -1;
+  const hipError_t st = hipGetDevice(&device);
+  if (st != hipSuccess) return st;
+  return done.once(device, [&]() {
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
+}
 
 typedef __bf16 bf16_t;
 typedef _Float16 f16_t;

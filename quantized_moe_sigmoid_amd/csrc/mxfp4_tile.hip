@@ -475,9 +475,8 @@ static hipError_t launch_tile(MxArgs a, int ny, hipStream_t s) {
   static_assert(S::BYTES <= 160 * 1024, "LDS");
   constexpr int BF = MODE == MX_GATEUP ? S::BN / 2 : S::BN;
   auto kernel = mx_tile_kernel<MODE, T, S, RAGGED>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
-  if (attr != hipSuccess) return attr;
+  static PerDevice allowed;
+  if (const hipError_t st = allow_lds(allowed, kernel, S::BYTES); st != hipSuccess) return st;
   a.strip = MODE == MX_LINEAR ? dense_strip(a.N, BF, ny, MX_CUS * S::OCC) : expert_strip<S>(a.K / 32);
   const unsigned groups = (unsigned)tile_strips(a.N, BF, a.strip) * (unsigned)ny;
   hipLaunchKernelGGL(kernel, dim3(MODE == MX_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);

@@ -29,26 +29,42 @@ namespace coli {
 // Loads of 64 lanes straight into LDS: 16 (4) bytes from each lane's address base + off to
 // consecutive LDS bytes at the wave-uniform address lds; the pair: two, 4096 LDS bytes apart
 // (the instruction's offset moves both addresses, so o0 is 4096 high). Lanes outside hi : lo
-// load nothing, and a load with an empty mask is counted like the others. Written as asm because
+// load nothing, and a load without lanes is counted like the others. Written as asm because
 // the compiler would wait for every such load before the next LDS read; the kernel counts them
-// itself. No register is loaded.
+// itself. No register is loaded; M0 and the active lanes are put back.
+__device__ __forceinline__ uint64_t lanes_of(int lo, int hi) {  // in scalar registers
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(hi) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane(lo);
+}
 __device__ __forceinline__ void dma16_pair(const uint8_t *base, uint32_t o0, uint32_t o1, uint32_t lds, int lo, int hi) {
+  uint64_t active;
+  uint32_t m0;
   asm volatile(
-      "s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\t"
-      "global_load_lds_dwordx4 %3, %5 offset:-4096\n\tglobal_load_lds_dwordx4 %4, %5\n\t"
-      "s_mov_b64 exec, -1" ::"s"(lds + 4096),
-      "s"(lo), "s"(hi), "v"(o0), "v"(o1), "s"(base)
-      : "memory");
+      "s_mov_b32 %1, m0\n\ts_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\t"
+      "global_load_lds_dwordx4 %4, %6 offset:-4096\n\tglobal_load_lds_dwordx4 %5, %6\n\t"
+      "s_mov_b32 m0, %1\n\ts_mov_b64 exec, %0"
+      : "=&s"(active), "=&s"(m0)
+      : "s"(lds + 4096), "s"(lanes_of(lo, hi)), "v"(o0), "v"(o1), "s"(base)
+      : "memory", "scc");
 }
 __device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int lo, int hi) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dwordx4 %3, %4\n\ts_mov_b64 exec, -1" ::"s"(lds),
-               "s"(lo), "s"(hi), "v"(off), "s"(base)
-               : "memory");
+  uint64_t active;
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %1, m0\n\ts_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\tglobal_load_lds_dwordx4 %4, %5\n\t"
+      "s_mov_b32 m0, %1\n\ts_mov_b64 exec, %0"
+      : "=&s"(active), "=&s"(m0)
+      : "s"(lds), "s"(lanes_of(lo, hi)), "v"(off), "s"(base)
+      : "memory", "scc");
 }
 __device__ __forceinline__ void dma4(const uint8_t *base, uint32_t off, uint32_t lds, int lo, int hi) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %1\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dword %3, %4\n\ts_mov_b64 exec, -1" ::"s"(lds),
-               "s"(lo), "s"(hi), "v"(off), "s"(base)
-               : "memory");
+  uint64_t active;
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %1, m0\n\ts_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\tglobal_load_lds_dword %4, %5\n\t"
+      "s_mov_b32 m0, %1\n\ts_mov_b64 exec, %0"
+      : "=&s"(active), "=&s"(m0)
+      : "s"(lds), "s"(lanes_of(lo, hi)), "v"(off), "s"(base)
+      : "memory", "scc");
 }
 
 template <int N>

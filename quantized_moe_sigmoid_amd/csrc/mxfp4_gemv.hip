@@ -13,10 +13,11 @@
 //
 // mx_down_kernel: the down product of few tokens (16 to a workgroup) with its weighted combine. A
 // workgroup (8 wavefronts) owns 8 to 32 output rows of its tokens and goes through all experts
-// they hold, a token to a column of the matrix instruction; the (expert, K group) units go to the
-// wavefronts in turn, two of each under way. No rows per pair are written, no second kernel sums
-// them. 16 tokens over 256 experts of 6144 x 2048: 118 us with the quantisation of h, 112 of them
-// this kernel (0.69 GB, 6.1 TB/s: the rate of a plain read). Three units under way: the same.
+// they hold, a token to a column of the matrix instruction; experts and K groups are dealt to the
+// wavefronts, one unit of each under way: with two the loads came in bursts (16 tokens over 256
+// experts of 6144 x 2048 118 us, over 64 of 4096 x 4096 100), with one 112 and 92. The pairs' rows
+// stay in LDS, no second kernel sums them. The 112 us have the quantisation of h in them: 0.69 GB,
+// 6.2 TB/s, the rate of a plain read. One token 15 us, 48 tokens 338.
 #include <cmath>
 
 #include "mxfp4_impl.h"
@@ -259,28 +260,55 @@ __global__ __launch_bounds__(256, 2) void mx_gemv_kernel(MxArgs a) {
 }
 
 // ------------------------------------------------------------------ down with its combine
-constexpr int DN_TOK = 16, DN_K = 16, DN_WAVES = 8, DN_DEPTH = 2;
+constexpr int DN_TOK = 16, DN_K = 16, DN_WAVES = 8;
+
+// Dynamic LDS of mx_down_kernel, bytes: slots first, then these; all but the quantised rows of ACT_X
+struct DownLds {
+  size_t list, y, x;
+};
+__host__ __device__ inline DownLds down_lds(const MxArgs &a, int step, int lp, int tokens) {
+  DownLds L;
+  L.list = (size_t)a.E * DN_TOK * 2;
+  L.y = L.list + ((size_t)tokens * a.k + 1 + 3) / 4 * 16;
+  L.x = L.y + ((size_t)tokens * (a.k + a.has_shared) << lp) * step * sizeof(float);
+  return L;
+}
+__host__ __device__ inline DownLds down_lds(const MxArgs &a, int step, int lp) {
+  return down_lds(a, step, lp, a.M < DN_TOK ? a.M : DN_TOK);
+}
 
 // RT 16-row tiles of the matrix instruction for the `step` output rows of a workgroup: rows past
 // them, like rows past N, read past their buffer's end, which gives zeros without an access.
+// 1 << lp wavefronts share an expert's K groups; what each sums for a (token, slot) has its own
+// place in LDS, and at the end the parts, then the weighted slots, then the shared expert's row
+// are added in order: a token's row does not depend on the tokens beside it.
 template <typename T, MxAct ACT, ScaleLoad SL, int RT>
-__global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int step, const int32_t *__restrict__ idx,
+__global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int step, int lp, const int32_t *__restrict__ idx,
                                                                const float *__restrict__ w, T *__restrict__ out) {
-  // slots[e * 16 + t]: the slots of token t that hold expert e, a bit each; the experts of the
-  // route; ACT_X: the quantised rows
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ float red[DN_WAVES][DN_TOK][16 * RT + 1];
-  uint16_t *slots = reinterpret_cast<uint16_t *>(lds);
+  __shared__ float weight[DN_TOK * DN_K];
+  __shared__ uint32_t there[DN_TOK];  // slots of a token that hold an expert, a bit each
+  __shared__ int n_entries, repeats;    // repeats: some token holds an expert in two slots
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lq = lane >> 4;
   const int n0 = blockIdx.x * step, nrows = min(step, a.N - n0);
   const int nb = a.K / 32, nbp = mx_padded(a.K) / 32, ng = nbp / 16;
   const int t0 = blockIdx.y * DN_TOK, T_ = min(DN_TOK, a.M - t0);  // this workgroup's tokens
-  const int k = a.k, E = a.E, P = a.M * k;
+  const int k = a.k, E = a.E, P = a.M * k, ks = k + a.has_shared;
+  // slots[e * 16 + t]: the slots of token t that hold expert e, a bit each; list: expert | round << 16 (a
+  // token that holds an expert in two slots takes another round of it); y: [token][slot][part][row];
+  // ACT_X: the quantised rows
+  const DownLds L = down_lds(a, step, lp);
+  uint16_t *slots = reinterpret_cast<uint16_t *>(lds);
+  int *list = reinterpret_cast<int *>(lds + L.list);
+  float *y = reinterpret_cast<float *>(lds + L.y);
+  uint8_t *lc = lds + L.x, *ls = lc;
+  static_assert(DN_TOK * DN_K <= 64 * DN_WAVES, "a thread for each slot");
+  const int my_e = tid < T_ * k ? idx[t0 * k + tid] : -1;
+  const float my_w = tid < T_ * k ? w[t0 * k + tid] : 0.0f;
   for (int i = tid; i < E * DN_TOK / 2; i += 64 * DN_WAVES) reinterpret_cast<uint32_t *>(slots)[i] = 0;
-  int *active = reinterpret_cast<int *>(lds + E * DN_TOK * 2);
-  __shared__ int n_active;
-  uint8_t *lc = lds + (E * (DN_TOK * 2 + 4) + 15) / 16 * 16, *ls = lc;
+  if (tid < DN_TOK) there[tid] = 0;
+  if (tid == 0) repeats = 0;
   if constexpr (ACT == ACT_X) {
     ls = lc + (P + a.has_shared) * nbp * 16;
     const T *x = static_cast<const T *>(a.x);
@@ -299,58 +327,58 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
     }
   }
   __syncthreads();
-  if (tid < T_)
-    for (int j = 0; j < k; j++) {
-      const int e = idx[(t0 + tid) * k + j];
-      if (e >= 0 && e < E) slots[e * DN_TOK + tid] |= (uint16_t)(1u << j);
-    }
-  __syncthreads();
-  if (wv == 0) {  // the experts that these tokens hold, in order
-    int n = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = min(e0 + lane, E - 1);
-      const uint4 x = reinterpret_cast<const uint4 *>(slots)[2 * e], y = reinterpret_cast<const uint4 *>(slots)[2 * e + 1];
-      const bool held = e0 + lane < E && (x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
-      const uint64_t who = __ballot(held);
-      if (held) active[n + __popcll(who & ((1ull << lane) - 1))] = e;
-      n += __popcll(who);
-    }
-    if (lane == 0) n_active = n;
+  if (my_e >= 0 && my_e < E) {
+    const int t = tid / k, j = tid - t * k;
+    const uint32_t at = 16 * (t & 1);
+    const uint32_t before = atomicOr(reinterpret_cast<uint32_t *>(slots) + (my_e * DN_TOK + t) / 2, 1u << (j + at));
+    if (before >> at & 0xFFFF) repeats = 1;
+    atomicOr(&there[t], 1u << j);
+    weight[tid] = my_w;
   }
   __syncthreads();
-  const int na = n_active, units = (na + a.has_shared) * ng;
+  if (wv == 0) {  // the experts that these tokens hold, in order, and the shared one
+    int n = 0;
+    const bool twice = __builtin_amdgcn_readfirstlane(repeats) != 0;
+    bool more = true;
+    for (int round = 0; more; round++) {
+      more = false;
+      for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = min(e0 + lane, E - 1);
+        const uint4 u = reinterpret_cast<const uint4 *>(slots)[2 * e], v = reinterpret_cast<const uint4 *>(slots)[2 * e + 1];
+        bool held = e0 + lane < E && (u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w) != 0;
+        if (twice) {
+          const uint32_t words[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+          int most = 0;  // slots of one token
+#pragma unroll
+          for (int i = 0; i < 8; i++) most = max(most, max(__popc(words[i] & 0xFFFF), __popc(words[i] >> 16)));
+          held = held && most > round;
+          more = more || __ballot(held && most > round + 1) != 0;
+        }
+        const uint64_t who = __ballot(held);
+        if (held) list[n + __popcll(who & ((1ull << lane) - 1))] = e | round << 16;
+        n += __popcll(who);
+      }
+    }
+    if (a.has_shared && lane == 0) list[n] = E;
+    if (lane == 0) n_entries = n + a.has_shared;
+  }
+  __syncthreads();
+  // this wavefront's entries: first, first + stride, ..; its K groups of each: part, part + parts, ..
+  const int parts = 1 << lp, part = wv & (parts - 1), first = wv >> lp, stride = DN_WAVES >> lp;
+  const int units = (__builtin_amdgcn_readfirstlane(n_entries) - first + stride - 1) / stride * ((ng - part + parts - 1) >> lp);
   const int rows = P + a.has_shared * a.M;
   v4f acc[RT] = {};
-  Group wg[DN_DEPTH][RT], act[DN_DEPTH];
-  uint32_t held[DN_DEPTH];  // slots of this lane's token that hold a unit's expert
-  float wt[DN_DEPTH];       // weight of the first
-  // A token's lanes take the row of its first slot of `mine` that holds expert e. A token without
-  // one (of 16 that pick 8 of 256 experts, 15 have none) reads past the buffer's end: zeros, and
-  // no access to the cache, whose rate this kernel would otherwise meet.
+  Group wg[RT], act;
+  int slot = -1;  // of this lane's token, that the unit is for, or -1
+  // A token's lanes take the row of the slot that holds the expert. A token without one (of 16 that
+  // pick 8 of 256 experts, 15 have none) reads past the buffer's end: zeros, and no access to the
+  // cache, whose rate this kernel would otherwise meet.
   [[maybe_unused]] const auto acr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(a.ac), 0, rows * nbp * 16, 0x00027000);
   [[maybe_unused]] const auto asr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(a.as), 0, rows * nbp, 0x00027000);
-  [[maybe_unused]] const auto wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(w), 0, P * 4, 0x00027000);
-  auto load_act = [&](int d, int e, int g, uint32_t mine) {
-    const int j = mine ? __builtin_ctz(mine) : 0, p = e < E ? (t0 + li) * k + j : P + t0 + li;
-    if constexpr (ACT == ACT_X) {
-      const int row = mine ? p : (e < E ? 0 : P);
-      load_group<SC_FULL>(lc + row * nbp * 16, ls + row * nbp, nbp, g, lq, act[d]);
-      wt[d] = !mine ? 0.0f : e < E ? w[p] : 1.0f;
-    } else {
-      const uint32_t row = (uint32_t)p * (uint32_t)nbp;
-      const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(asr, mine ? row + g * 16 : ~0u, 0, 0));
-      act[d].u[0] = u.x, act[d].u[1] = u.y, act[d].u[2] = u.z, act[d].u[3] = u.w;
-#pragma unroll
-      for (int s = 0; s < 4; s++)
-        act[d].c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(acr, mine ? (row + g * 16 + 4 * s + lq) * 16 : ~0u, 0, 0));
-      const float v = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(wr, mine && e < E ? p * 4 : ~0u, 0, 0));
-      wt[d] = e < E ? v : 1.0f;
-    }
-  };
-  // weights and activations of a unit together, since loads arrive in order
-  auto load = [&](int d, int u) {
-    const int s = u / ng, g = u - s * ng;
-    const int e = s < na ? __builtin_amdgcn_readfirstlane(active[s]) : E;
+  // weights and activations of the next unit together, since loads arrive in order
+  int at = first, g = part;
+  auto load = [&]() {
+    const int entry = __builtin_amdgcn_readfirstlane(list[at]), e = entry & 0xFFFF;
     const auto wc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t *>(a.wc) + (int64_t)e * a.wc_stride + (int64_t)n0 * nb * 16, 0, nrows * nb * 16, 0x00027000);
     const auto ws = __builtin_amdgcn_make_buffer_rsrc(
@@ -360,59 +388,81 @@ __global__ __launch_bounds__(64 * DN_WAVES) void mx_down_kernel(MxArgs a, int st
       const uint32_t row = (uint32_t)(16 * i + li) * (uint32_t)nb;
       if constexpr (SL != SC_BYTES) {
         const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ws, row + min(g * 16, nb - 16), 0, 0));
-        wg[d][i].u[0] = u.x, wg[d][i].u[1] = u.y, wg[d][i].u[2] = u.z, wg[d][i].u[3] = u.w;
+        wg[i].u[0] = u.x, wg[i].u[1] = u.y, wg[i].u[2] = u.z, wg[i].u[3] = u.w;
       }
 #pragma unroll
       for (int s = 0; s < 4; s++) {
         const int b = min(g * 16 + 4 * s + lq, nb - 1);  // past K: activations of zero
-        wg[d][i].c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wc, (row + b) * 16, 0, 0));
-        if constexpr (SL == SC_BYTES) wg[d][i].u[s] = __builtin_amdgcn_raw_buffer_load_b8(ws, row + b, 0, 0);
+        wg[i].c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wc, (row + b) * 16, 0, 0));
+        if constexpr (SL == SC_BYTES) wg[i].u[s] = __builtin_amdgcn_raw_buffer_load_b8(ws, row + b, 0, 0);
       }
     }
-    held[d] = li < T_ ? (e < E ? slots[e * DN_TOK + li] : 1u) : 0u;
-    load_act(d, e, g, held[d]);
+    uint32_t mine = li < T_ ? (e < E ? slots[e * DN_TOK + li] : 1u) : 0u;
+    for (int i = entry >> 16; i > 0; i--) mine &= mine - 1;
+    const int j = mine ? (e < E ? __builtin_ctz(mine) : k) : -1, p = j < k ? (t0 + li) * k + j : P + t0 + li;
+    slot = j;
+    if constexpr (ACT == ACT_X) {
+      const int row = mine ? p : 0;
+      load_group<SC_FULL>(lc + row * nbp * 16, ls + row * nbp, nbp, g, lq, act);
+    } else {
+      const uint32_t row = (uint32_t)p * (uint32_t)nbp;
+      const uint4 u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(asr, mine ? row + g * 16 : ~0u, 0, 0));
+      act.u[0] = u.x, act.u[1] = u.y, act.u[2] = u.z, act.u[3] = u.w;
+#pragma unroll
+      for (int s = 0; s < 4; s++)
+        act.c[s] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(acr, mine ? (row + g * 16 + 4 * s + lq) * 16 : ~0u, 0, 0));
+    }
+    g += parts;
+    if (g >= ng) g = part, at += stride;
   };
+  if (units > 0) load();
+  int cg = part;  // K group of the unit that is multiplied
+  for (int u = 0; u < units; u++) {
 #pragma unroll
-  for (int d = 0; d < DN_DEPTH; d++)
-    if (wv + DN_WAVES * d < units) load(d, wv + DN_WAVES * d);
-  for (int u0 = wv; u0 < units; u0 += DN_WAVES * DN_DEPTH) {
+    for (int i = 0; i < RT; i++) {
+      end_group<SL>(wg[i], nb, cg);
 #pragma unroll
-    for (int d = 0; d < DN_DEPTH; d++) {
-      const int u = u0 + DN_WAVES * d;
-      if (u < units) {
-        uint32_t mine = held[d];
+      for (int s = 0; s < 4; s++)  // rows of the result: weight rows; columns: tokens
+        acc[i] = mx_mfma16(wg[i].c[s], group_scale<SL>(wg[i], s, lq), act.c[s], group_scale<SC_FULL>(act, s, lq), acc[i]);
+    }
+    cg += parts;
+    if (cg >= ng) {  // the expert is done
+      cg = part;
 #pragma unroll
-        for (int i = 0; i < RT; i++) end_group<SL>(wg[d][i], nb, u % ng);
-        while (true) {
-#pragma unroll
-          for (int i = 0; i < RT; i++) {
-            v4f dsum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < 4; s++)  // rows of the result: weight rows; columns: tokens
-              dsum = mx_mfma16(wg[d][i].c[s], group_scale<SL>(wg[d][i], s, lq), act[d].c[s], group_scale<SC_FULL>(act[d], s, lq), dsum);
-#pragma unroll
-            for (int r = 0; r < 4; r++) acc[i][r] = mine ? __builtin_fmaf(wt[d], dsum[r], acc[i][r]) : acc[i][r];
-          }
-          // a token holds an expert in one slot; a route that repeats one takes another round
-          mine &= mine - 1;
-          if (__builtin_expect(__ballot(mine != 0) == 0, 1)) break;
-          const int s = u / ng;
-          load_act(d, active[s], u - s * ng, mine);  // (the shared expert is held once)
-        }
-        if (u + DN_WAVES * DN_DEPTH < units) load(d, u + DN_WAVES * DN_DEPTH);
+      for (int i = 0; i < RT; i++) {
+        if (slot >= 0 && 16 * i + 4 * lq < step)
+          *reinterpret_cast<v4f *>(y + (((li * ks + slot) << lp) + part) * step + 16 * i + 4 * lq) = acc[i];
+        acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
       }
     }
+    if (u + 1 < units) load();
   }
-#pragma unroll
-  for (int i = 0; i < RT; i++)
-#pragma unroll
-    for (int r = 0; r < 4; r++) red[wv][li][16 * i + 4 * lq + r] = acc[i][r];
   __syncthreads();
   const int t = tid / (16 * RT), r = tid % (16 * RT);
   if (t < T_ && r < nrows) {
+    const uint32_t some = there[t];
     float s = 0.f;
+    auto add = [&]<int PARTS>() {
+      auto row = [&](int j) {
+        const float *v = y + (t * ks + j) * PARTS * step + r;
+        float sum = v[0];
 #pragma unroll
-    for (int i = 0; i < DN_WAVES; i++) s += red[i][t][r];
+        for (int i = 1; i < PARTS; i++) sum += v[i * step];
+        return sum;
+      };
+#pragma unroll 4
+      for (int j = 0; j < k; j++) {
+        const float v = row(j);  // of an empty slot: whatever is there
+        s = some >> j & 1 ? __builtin_fmaf(weight[t * k + j], v, s) : s;
+      }
+      if (a.has_shared) s += row(k);
+    };
+    switch (lp) {
+      case 0: add.template operator()<1>(); break;
+      case 1: add.template operator()<2>(); break;
+      case 2: add.template operator()<4>(); break;
+      default: add.template operator()<8>();
+    }
     out[(int64_t)(t0 + t) * a.N + n0 + r] = (T)s;
   }
 }
@@ -430,16 +480,31 @@ static int down_step(int N) {
   return best;
 }
 
-// LDS of mx_down_kernel, and of its rows when it quantises them itself
-static size_t down_lds(const MxArgs &a, bool x) {
-  const size_t nbp = mx_padded(a.K) / 32;
-  return ((size_t)a.E * (DN_TOK * 2 + 4) + 15) / 16 * 16 + (x ? ((size_t)a.M * a.k + (size_t)a.M * a.has_shared) * nbp * 17 : 0);
+// Wavefronts (1 << lp) to an expert's K groups: so many that one token's experts end soonest, and
+// the finer cut of two, which evens out a batch's (16 tokens over 64 experts of 4096 x 1920, 6 to a
+// token: 42 us against 46.5 with whole experts; of 4096 x 4096, 8 to a token: 92 against 103), as
+// far as the LDS of two workgroups to a CU goes. Nothing of the batch enters: the parts order the sums.
+constexpr size_t DN_LDS = 80 * 1024;
+static int down_parts(const MxArgs &a, int step) {
+  const int ng = mx_padded(a.K) / 512, n = a.k + a.has_shared;
+  int best = 0, cost = 1 << 30;
+  for (int lp = 0; 1 << lp <= DN_WAVES && 1 << lp <= ng; lp++) {
+    if (lp > 0 && down_lds(a, step, lp, DN_TOK).x > DN_LDS) break;
+    const int lanes = DN_WAVES >> lp, c = (n + lanes - 1) / lanes * ((ng + (1 << lp) - 1) >> lp);
+    if (c <= cost) cost = c, best = lp;
+  }
+  return best;
+}
+
+// The rows of one token in LDS, when mx_down_kernel quantises them itself
+static size_t down_rows_lds(const MxArgs &a) {
+  return ((size_t)a.M * a.k + (size_t)a.M * a.has_shared) * (mx_padded(a.K) / 32) * 17;
 }
 
 // More than 16 tokens go through the weights of their experts once for each 16: worth it while
 // that reads less than 1.7 times the distinct experts of an even route. Of 256 experts of
-// 6144 x 2048, 8 to a token: 24 tokens 267 -> 188 us, 32 323 -> 237 (1.27 times), 48 398 -> 354
-// (1.55 times); 64 (1.85 times) about 450 against 438.
+// 6144 x 2048, 8 to a token: 24 tokens 267 -> 180 us, 32 323 -> 228 (1.27 times), 48 398 -> 338
+// (1.55 times), 56 429 -> 396 (1.71 times, not taken); 64 (1.85 times) 450 and 445: no gain.
 bool mx_down_fused(const MxArgs &a) {
   if (a.k > DN_K) return false;
   if (a.M <= DN_TOK) return true;
@@ -447,8 +512,7 @@ bool mx_down_fused(const MxArgs &a) {
   auto hit = [&](int tokens) { return 1.0 - std::pow(1.0 - (double)a.k / a.E, tokens); };
   return a.M / DN_TOK * hit(DN_TOK) + hit(a.M % DN_TOK) <= 1.7 * hit(a.M);
 }
-// (the dynamic part of 64 KB; the sums have the rest)
-bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && down_lds(a, true) <= 46 * 1024; }
+bool mx_down_from_x(const MxArgs &a) { return a.M == 1 && (size_t)a.E * (DN_TOK * 2 + 4) + down_rows_lds(a) <= 46 * 1024; }
 // One row quantised by every workgroup
 bool mx_gemv_from_x(const MxArgs &a) { return a.M == 1 && mx_padded(a.K) / 32 * 17 <= 48 * 1024; }
 
@@ -500,28 +564,27 @@ hipError_t launch_mx_gemv(MxMode mode, int dtype, const MxArgs &a, hipStream_t s
 
 template <typename T>
 static hipError_t launch_down_t(const MxArgs &a, const int32_t *idx, const float *w, void *out, hipStream_t s) {
-  const int step = down_step(a.N);
+  const int step = down_step(a.N), lp = down_parts(a, step);
   const dim3 g((unsigned)((a.N + step - 1) / step), (unsigned)((a.M + DN_TOK - 1) / DN_TOK)), b(64 * DN_WAVES);
-  const size_t lds = down_lds(a, a.x != nullptr);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, g, b, lds, s, a, step, idx, w, (T *)out); };
+  const size_t lds = down_lds(a, step, lp).x + (a.x ? down_rows_lds(a) : 0);
+  auto go = [&]<MxAct ACT, ScaleLoad SL, int RT>() {
+    static PerDevice allowed;
+    auto kernel = mx_down_kernel<T, ACT, SL, RT>;
+    if (const hipError_t st = allow_lds(allowed, kernel, 144 * 1024); st != hipSuccess) return st;
+    hipLaunchKernelGGL(kernel, g, b, lds, s, a, step, lp, idx, w, (T *)out);
+    return hipGetLastError();
+  };
   auto pick = [&]<MxAct ACT, ScaleLoad SL>() {
-    if (step <= 16)
-      go(mx_down_kernel<T, ACT, SL, 1>);
-    else
-      go(mx_down_kernel<T, ACT, SL, 2>);
+    return step <= 16 ? go.template operator()<ACT, SL, 1>() : go.template operator()<ACT, SL, 2>();
   };
   auto with_x = [&]<ScaleLoad SL>() {
-    if (a.x)
-      pick.template operator()<ACT_X, SL>();
-    else
-      pick.template operator()<ACT_WS, SL>();
+    return a.x ? pick.template operator()<ACT_X, SL>() : pick.template operator()<ACT_WS, SL>();
   };
   switch (scale_load(a)) {
-    case SC_FULL: with_x.template operator()<SC_FULL>(); break;
-    case SC_ANY: with_x.template operator()<SC_ANY>(); break;
-    default: with_x.template operator()<SC_BYTES>();
+    case SC_FULL: return with_x.template operator()<SC_FULL>();
+    case SC_ANY: return with_x.template operator()<SC_ANY>();
+    default: return with_x.template operator()<SC_BYTES>();
   }
-  return hipGetLastError();
 }
 
 hipError_t launch_mx_down(const MxArgs &a, const int32_t *idx, const float *w, void *out, int dtype, hipStream_t s) {

@@ -594,3 +594,57 @@ def test_experts_odd_stages_of_several_column_tiles(q, K):
     """Rows of 3, 5, 7 and 9 stages of 256 inputs, several column tiles, tokens past one row tile."""
     test_gate_up(q, (300, K, 512, 8, 2, True, 0, False), "bfloat16")
     test_down(q, (300, 1024, K, 8, 2, True, 0, False), "bfloat16")
+
+
+@pytest.mark.parametrize("T,H,F,E,k", [(2, 256, 2048, 64, 8), (16, 640, 2048, 64, 8), (16, 256, 1152, 16, 3),
+                                       (40, 384, 1024, 8, 2), (90, 256, 640, 16, 8)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_down_row_whatever_its_neighbours(q, T, H, F, E, k, shared):
+    """A token's down row is the same bits whichever experts the tokens beside it hold."""
+    import torch
+    rng, cfg, weights, idx, w, _, _, _ = _setup(q, (T, H, F, E, k, shared, 0, False), T + F)
+    h = _t(rng.standard_normal((T * (k + shared), F)).astype(np.float32))
+    ws = q.alloc_mxfp4_experts_workspace(cfg, T)
+    rows = []
+    for i in range(6):
+        other, _ = _route_of(np.random.default_rng(i), T, E, k, 0.3 if i else 0, False)
+        other[T // 2] = idx[T // 2]
+        perm, off, act, na = mxref.group(other, E)
+        out = torch.empty((T, H), device="cuda")
+        q.mxfp4_down(cfg, weights, h, _t(other), _t(w), *[_t(a) for a in (off, perm, act, na)], out, ws)
+        rows.append(out[T // 2].clone())
+    assert all(torch.equal(r, rows[0]) for r in rows)
+
+
+@pytest.mark.parametrize("T,H,F,E,k", [(1, 256, 128, 8, 4), (1, 384, 2048, 64, 8), (3, 5248, 640, 16, 5), (16, 640, 512, 64, 8),
+                                       (16, 256, 1152, 8, 3), (20, 384, 2048, 8, 4), (90, 256, 640, 16, 8), (300, 256, 384, 8, 2)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_down_adds_in_slot_order(q, T, H, F, E, k, shared):
+    """Rows that are exact and weights of powers of two: the sum over slots, then the shared expert's
+    row, rounded to fp32 at every step, bit for bit. Empty slots and repeated experts among them."""
+    import torch
+    rng = np.random.default_rng(T * F + k)
+    idx, _ = _route_of(rng, T, E, k, 0.1, False)
+    if k > 2:
+        idx[::3, k - 1] = idx[::3, 0]  # an expert in two slots
+    w = np.exp2(rng.integers(-18, 19, (T, k))).astype(np.float32)
+    cfg = q.make_cfg(H, F, E, k, has_shared=shared, wbits=q.W_MXFP4, scale_group=32)
+    codes = rng.integers(0, 256, (E + shared, 3, F * H // 2), dtype=np.uint8)
+    scales = np.full((E + shared, 3, F * H // 32), 127, np.uint8)
+    x = mxref.E2M1[rng.integers(0, 16, (T * (k + shared), F))]
+    x[:, ::32] = 6.0  # a block's power of two is 1: every sum of a row is a multiple of 1/4 below 2^22
+    perm, off, act, na = mxref.group(idx, E)
+    out = torch.empty((T, H), device="cuda")
+    q.mxfp4_down(cfg, q.Weights(_t(codes.reshape(E + shared, -1)), _t(scales.reshape(E + shared, -1)), None, None),
+                 _t(x.astype(np.float32)), _t(idx), _t(w), *[_t(a) for a in (off, perm, act, na)], out,
+                 q.alloc_mxfp4_experts_workspace(cfg, T))
+    y = np.zeros((T * (k + shared), H), np.float32)
+    for e, p, _ in _rows_of(idx, T, k, shared, E):
+        y[p] = x[p] @ _mats(codes, scales, e, 2, H).T
+    want = np.zeros((T, H), np.float32)
+    for j in range(k):
+        there = idx[:, j] >= 0
+        want[there] += (w[there, j, None] * y[:T * k].reshape(T, k, H)[there, j])
+    if shared:
+        want += y[T * k:]
+    assert np.array_equal(out.cpu().numpy(), want)

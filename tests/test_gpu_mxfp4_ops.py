@@ -648,3 +648,44 @@ def test_down_adds_in_slot_order(q, T, H, F, E, k, shared):
     if shared:
         want += y[T * k:]
     assert np.array_equal(out.cpu().numpy(), want)
+
+
+EXPERTS_LIMITS = [  # most slots of the kernel for few tokens and more than it takes, most experts
+    (1, 256, 128, 24, 16, True, 0, False), (16, 128, 640, 24, 16, True, 0.1, False), (40, 256, 128, 32, 16, False, 0, False),
+    (1, 128, 256, 24, 20, True, 0, False), (16, 256, 128, 24, 20, False, 0.1, False), (40, 128, 128, 24, 20, True, 0, False),
+    (1, 128, 128, 1024, 8, True, 0, False), (16, 256, 128, 1024, 16, True, 0, False), (600, 128, 128, 1024, 2, True, 0.1, True),
+    (9, 128, 128, 64, 64, False, 0.2, False),
+]
+
+
+@pytest.mark.parametrize("case", EXPERTS_LIMITS, ids=str)
+def test_gate_up_limits(q, case):
+    test_gate_up(q, case, "bfloat16")
+
+
+@pytest.mark.parametrize("case", EXPERTS_LIMITS, ids=str)
+def test_down_limits(q, case):
+    test_down(q, case, "bfloat16")
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+def test_experts_scales_at_any_dword(q, T):
+    """Scales that start 4 bytes past a 16-byte address: the results of aligned ones, bit for bit."""
+    import torch
+    H, F, E, k = 512, 512, 8, 2
+    rng, cfg, weights, idx, w, grouping, _, _ = _setup(q, (T, H, F, E, k, True, 0, False), T)
+    moved = torch.empty(weights.scales.numel() + 16, dtype=torch.uint8, device="cuda")
+    at = (4 - moved.data_ptr()) % 16
+    moved = moved[at:at + weights.scales.numel()].view(weights.scales.shape)
+    moved.copy_(weights.scales)
+    assert moved.data_ptr() % 16 == 4 and weights.scales.data_ptr() % 16 == 0
+    x, h = _t(rng.standard_normal((T, H)).astype(np.float32)), _t(rng.standard_normal((T * (k + 1), F)).astype(np.float32))
+    ws = q.alloc_mxfp4_experts_workspace(cfg, T)
+    got = []
+    for scales in (weights.scales, moved):
+        wt = q.Weights(weights.experts, scales, None, None)
+        hh, out = torch.empty((T * (k + 1), F), device="cuda"), torch.empty((T, H), device="cuda")
+        q.mxfp4_gate_up(cfg, wt, x, *grouping, hh, ws)
+        q.mxfp4_down(cfg, wt, h, _t(idx), _t(w), *grouping, out, ws)
+        got.append((hh, out))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

@@ -92,13 +92,14 @@ __device__ __forceinline__ v4f mx_mfma16(uint4 a, uint32_t ua, uint4 b, uint32_t
 
 // silu in fp32 for the many values of a tile: e^-g = 2^h (1 + l ln 2) with h + l = -g log2(e)
 // to about 2^-46, by the hardware's exponential and reciprocal (within 1 ulp each). The clamp
-// keeps h + l finite: below it 1 + e^-g is 1, above it infinite.
+// keeps h + l finite: below it 1 + e^-g is 1, above it infinite. The reciprocal of 1 + e^-g past
+// 2^126 would count as 0 while e^-g is still finite (g from -88.7 to -87.3), so 2^-8 of it is taken.
 __device__ __forceinline__ float silu_fast(float g) {
   const float x = __builtin_amdgcn_fmed3f(-g, -126.0f, 200.0f);
   const float h = x * 0x1.715476p+0f;
   const float l = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -h));
   const float e = __builtin_amdgcn_exp2f(h) * __builtin_fmaf(l, 0x1.62e430p-1f, 1.0f);
-  return g * __builtin_amdgcn_rcpf(1.0f + e);
+  return g * 0x1p-8f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0x1p-8f, 0x1p-8f));
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }

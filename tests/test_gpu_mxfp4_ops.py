@@ -689,3 +689,33 @@ def test_experts_scales_at_any_dword(q, T):
         q.mxfp4_down(cfg, wt, h, _t(idx), _t(w), *grouping, out, ws)
         got.append((hh, out))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("T", [1, 8, 300])
+def test_gate_up_gates_near_the_exponentials_end(q, T):
+    """Gates from -80 to -88.6, whose e^-g is still a finite fp32 value: g / (1 + e^-g) is not 0 there."""
+    import torch
+    H, F, E, k = 128, 128, 4, 2
+    codes = np.zeros((3, F, H), np.uint8)
+    steps = 640 + np.arange(F) % 70  # -8 g, as a sum of E2M1 values of weight 2^-3
+    for f in range(F):
+        left, i = steps[f], 0
+        while left:
+            c, v = next((c, v) for c, v in ((7, 6), (6, 4), (5, 3), (4, 2), (2, 1)) if v <= left)
+            codes[0, f, i] = c | 8
+            left, i = left - v, i + 1
+    codes[1, :, 0] = 2  # every up value 1
+    blocks = codes.reshape(3, F, H // 32, 32)
+    packed = (blocks[..., :16] | (blocks[..., 16:] << 4)).reshape(3, -1)
+    scales = np.full((3, F * H // 32), 127, np.uint8)
+    scales[0] = 124
+    cfg = q.make_cfg(H, F, E, k, has_shared=False, wbits=q.W_MXFP4, scale_group=32)
+    w = q.Weights(_t(np.stack([packed.reshape(-1)] * E)), _t(np.stack([scales.reshape(-1)] * E)), None, None)
+    perm, off, act, na = mxref.group(np.tile(np.array([[0, 3]], np.int32), (T, 1)), E)
+    h = torch.empty((T * k, F), device="cuda")
+    q.mxfp4_gate_up(cfg, w, torch.ones((T, H), device="cuda"), *[_t(a) for a in (off, perm, act, na)], h,
+                    q.alloc_mxfp4_experts_workspace(cfg, T))
+    g = -steps / 8.0  # exact in fp32 in any order
+    want = g / (1 + np.exp(-g))
+    # exp, sum, division, product: four steps each of at most 2 ulp
+    assert (np.abs(_n(h) - want) <= 8 * 2.0 ** -23 * np.abs(want)).all()

@@ -83,7 +83,20 @@ static MxArgs expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
 
 static hipError_t launch_experts(MxMode mode, int dtype, MxArgs &a, uint8_t *ws, const MxWs &L, hipStream_t s) {
   a.ws_pitch = a.K / 32;
-  // the tiled kernel's offsets into the activations and the output have 32 bits
+  // The kernel for few rows up to 512 pairs (decode batches), the tiled one past them. What makes
+  // the difference is rows to an expert, the shared one's among them: the first kernel reads the
+  // weights once for each 16, the second takes at least a whole tile's time. us, few rows and tiled:
+  //   experts of 4096 x 2048            gate/up            down (few rows: pairs, combine)
+  //   8, 1 to a token: 64 tokens        21 and 30          19 and 22
+  //     128 tokens                      33 and 30          23 and 23
+  //     500 tokens                      75 and 42          53 and 33
+  //     500, with a shared expert       157 and 44         82 and 38
+  //   16, 2 to a token: 64 tokens       38 and 40          29 and 23
+  //     250 tokens                      82 and 43          56 and 28
+  //   64, 8 to a token: 64 tokens       139 and 107        102 and 70
+  //   256 of 6144 x 2048, 8: 64 tokens  543 and 533        441 and 292
+  // So the bound by pairs is right where an expert has up to about 16 rows, and late for few experts.
+  // The tiled kernel's offsets into the activations and the output have 32 bits.
   const int64_t rows = (int64_t)a.M * (a.k + a.has_shared), widest = std::max<int64_t>((int64_t)a.N * 4, mx_padded(a.K) / 2);
   if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P || rows * widest >= ((int64_t)1 << 32) - 65536)
     return launch_mx_gemv(mode, dtype, a, s);

@@ -5,8 +5,9 @@
 //
 // Bound by memory: a value is read once and 17/32 byte of it written (and the reverse). Two
 // lanes own a block, so every load is 16 bytes wide and every store of codes 8 bytes. 49152 x 2048
-// bf16: 58 us to codes (254 MB, 4.4 TB/s), 39 us back (6.5 TB/s), copies reaching 4.7 to 4.9;
-// two or four blocks to a thread: 2 to 5 us slower.
+// bf16 on buffers that no cache holds: 44 us to codes (254 MB, 5.8 TB/s), 46 us back (5.5 TB/s); a
+// plain read reaches 6.4 TB/s, a fill 6.9, a copy 5.2. The same buffers again and again, partly
+// from the last-level cache: 35 and 38 us. Two or four blocks to a thread: 2 to 5 us slower.
 #include "mxfp4_impl.h"
 
 namespace coli {

@@ -5,7 +5,7 @@
 // y = sum over blocks of 2^(ua - 127) 2^(uw - 127) sum a_i w_i: the instruction takes both
 // operands' codes and their E8M0 bytes, so a block costs no work of the vector units.
 //
-// Dense, M = 4096, N = 12288, K = 6144 bf16: 177 to 195 us (3.2 to 3.5 PFLOP/s). The instruction
+// Dense, M = 4096, N = 12288, K = 6144 bf16: 178 to 185 us (3.3 to 3.5 PFLOP/s). The instruction
 // on random codes in registers alone reaches 6.1 to 6.4 PFLOP/s here (9.2 on zeros: the card's
 // power, not the issue rate, is the limit), which is 100 us; without its products the kernel
 // takes 145, without scales too 132: the tile's way through L2 and LDS and the matrix cores each
@@ -13,7 +13,7 @@
 // full rate, close to what whole 128-byte lines reach (36; 64-byte pieces 22), hence stages of
 // 256 inputs, one row of a stage to a line. A wavefront's 128 x 128 part fills the accumulators.
 //
-// Over a route, 2048 tokens, 256 experts of 6144 x 2048, Zipf-like: gate/up 811 us, down 480 (and
+// Over a route, 2048 tokens, 256 experts of 6144 x 2048, Zipf-like: gate/up 815 us, down 480 (and
 // 96 for the combine). Bound by the weights' way from HBM: 3.4 GB, of which the kernel fetches
 // 3.9 (a line of scale bytes comes back for every two stages). Measured when the whole took 825:
 // without products 804, without scales 749; 8 wavefronts to the tile 851 (with two stages in LDS

@@ -294,6 +294,83 @@ int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, cons
                         const int32_t *pair_perm, const int32_t *active, const int32_t *n_active, void *out,
                         void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- Products in 8-bit integers with scales for each token and channel ----
+ * The integer-dot product (colibri-strix README, "What's implemented", integer-dot kernels item)
+ * with one activation scale for a whole row, where Q8_0 has one for each 32 values: the sums stay
+ * in integers over all of K. Conventions and element types as above. Activations are quantised
+ * inside the products:
+ *   int8 of a row x: s = max|x| / 127 (one fp32 division), codes q = x / s (one fp32 division)
+ *   rounded to nearest, halves away from zero, clamped to [-127, 127]; s = 0 gives q = 0. A row
+ *   that holds an infinity or a NaN has s = NaN and codes 0.
+ * acc = sum_k q_k w_k is exact (int32); a product is (float)acc * (s_row * s_channel), so that it
+ * depends neither on the batch nor on the kernel that a size takes. Outputs are rounded once. */
+
+/* int8 of rows x cols values (cols % 16 == 0, cols <= 2^17; x and codes 16-byte aligned): codes
+ * [rows][cols], scales fp32 [rows]. rows < 2^31, rows * cols < 2^40. */
+int coli_moe_int8_quantize(const void *x, int dtype, int64_t rows, int32_t cols, int8_t *codes, float *scales,
+                           void *stream);
+
+/* y [M][N] = int8(x [M][K]) W^T + bias, W's N rows given as codes int8 [N][K] (16-byte aligned) and
+ * scales fp32 [N]; bias fp32 [N] or NULL. K % 16 == 0, K <= 2^17, M, N <= 2^20, M * K and N * K < 2^37,
+ * x and y 16-byte aligned, y of x's dtype. workspace: coli_moe_int8_linear_workspace_bytes(M_max, N, K),
+ * 256-byte aligned, for every M <= M_max (0 if a size is invalid; M = 0 or N = 0: a no-op). */
+size_t coli_moe_int8_linear_workspace_bytes(int32_t M_max, int32_t N, int32_t K);
+int coli_moe_int8_linear(const void *x, int dtype, const int8_t *codes, const float *scales, const float *bias, int32_t M,
+                         int32_t N, int32_t K, void *y, void *workspace, size_t ws_bytes, void *stream);
+
+/* The two halves of the expert FFN over a route and its grouping (coli_moe_group's or
+ * coli_moe_sort_pairs' arrays for the same T), with the experts of coli_moe_ffn: cfg->wfmt =
+ * COLI_W_INT8, scale_group 0. Shapes, empty slots, the shared expert and the sums are those of
+ * coli_moe_mxfp4_gate_up and _down; h is quantised row by row. workspace:
+ * coli_moe_int8_experts_workspace_bytes(cfg, T_max) (0 if invalid), 256-byte aligned, for either
+ * half and every T <= T_max.
+ * Follow the batch-union item of colibri-strix README, "What's implemented". */
+size_t coli_moe_int8_experts_workspace_bytes(const coli_moe_cfg *cfg, int32_t T_max);
+int coli_moe_int8_gate_up(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *x, int dtype, int32_t T,
+                          const int32_t *expert_off, const int32_t *pair_perm, const int32_t *active,
+                          const int32_t *n_active, void *h, void *workspace, size_t ws_bytes, void *stream);
+int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *h, int dtype, int32_t T,
+                       const int32_t *topk_idx, const float *topk_w, const int32_t *expert_off,
+                       const int32_t *pair_perm, const int32_t *active, const int32_t *n_active, void *out,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- Pairs to their experts and back, and the gradients ----
+ * For experts whose products lie elsewhere (another library's, other devices', a training step's).
+ *   sort_pairs: coli_moe_group's expert_off, pair_perm, active and n_active for any number of pairs
+ *     P = T k < 2^30 (n_experts <= 1024), and pair_pos int32 [P], the place of every pair in
+ *     pair_perm, -1 for an empty slot. workspace: coli_moe_sort_pairs_workspace_bytes(P, n_experts)
+ *     (0 if invalid), 256-byte aligned, enough for fewer pairs too.
+ *   dispatch: xs [rows][H], row pair_pos[t k + j] = x row t, bit for bit. x [T][H].
+ *   combine: out [T][H], out_t = sum_j w_tj ys[pair_pos[t k + j]] in slot order + add_t, in fp32 and
+ *     rounded once. topk_w fp32 [T][k] or NULL (weights 1), add [T][H] or NULL. Without weights
+ *     it is the gradient of dispatch; dispatch is the gradient of combine without weights.
+ *   combine_backward: from dout [T][H] and the ys of combine: dys [rows][H], row pair_pos[t k + j] =
+ *     w_tj dout_t, and dtopk_w fp32 [T][k], w_tj's gradient <dout_t, ys row> summed in fp32 (0 for an
+ *     empty slot). dys or dtopk_w may be NULL: not wanted. ys may be NULL without dtopk_w.
+ * A place outside [0, rows) is an empty slot; rows that no pair has are not written (so rows may be
+ * more than the pairs). A place may stand once. xs, ys, x, out, add, dout and dys of one dtype, any H,
+ * aligned to their type (16 bytes and H a multiple of 16 bytes run faster); T k < 2^30, T H < 2^40. */
+size_t coli_moe_sort_pairs_workspace_bytes(int64_t P, int32_t n_experts);
+int coli_moe_sort_pairs(const int32_t *topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t *expert_off,
+                        int32_t *pair_perm, int32_t *pair_pos, int32_t *active, int32_t *n_active, void *workspace,
+                        size_t ws_bytes, void *stream);
+int coli_moe_dispatch(const void *x, int dtype, int32_t T, int32_t k, int32_t H, const int32_t *pair_pos, int64_t rows,
+                      void *xs, void *stream);
+int coli_moe_combine(const void *ys, int dtype, int64_t rows, int32_t T, int32_t k, int32_t H, const int32_t *pair_pos,
+                     const float *topk_w, const void *add, void *out, void *stream);
+int coli_moe_combine_backward(const void *dout, const void *ys, int dtype, int64_t rows, int32_t T, int32_t k, int32_t H,
+                              const int32_t *pair_pos, const float *topk_w, void *dys, float *dtopk_w, void *stream);
+
+/* The gradient of coli_moe_route_logits: dz [T][E] (of z's dtype) from dtopk_w fp32 [T][k], for the
+ * experts topk_idx that it took (-1: none; they are held fixed, as is every expert's presence). With
+ * p = sigmoid(z) or softmax(z), a_j = scale * dtopk_w_j, or with renorm scale * (dtopk_w_j -
+ * sum_i dtopk_w_i p_i / S) / S for the sum S of the taken p (0 where S is 0):
+ *   sigmoid: dz_e = a_e p_e (1 - p_e); softmax: dz_e = p_e (a_e - sum_i a_i p_i), the sum 0 with
+ * renorm; a_e of an expert that was not taken is 0, of one in two slots their sum. Absent experts
+ * and logits of +inf have 0. In fp64, rounded once. dz may be z. T < 2^26 - 3. */
+int coli_moe_route_logits_backward(const coli_moe_router *r, const void *z, int dtype, int32_t T, const int32_t *topk_idx,
+                                   const float *dtopk_w, void *dz, void *stream);
+
 /* Static text for a status code. */
 const char *coli_moe_strerror(int status);
 

@@ -9,6 +9,9 @@ Entry points (same names as the C ABI in include/coli_moe.h):
     blob_bytes, workspace_bytes, scratch_bytes, num_stages, stage_name, strerror;
     route_logits, mxfp4_quantize, mxfp4_dequantize, mxfp4_linear, mxfp4_gate_up,
     mxfp4_down (with make_router and the alloc_mxfp4_*_workspace helpers);
+    int8_quantize, int8_linear, int8_gate_up, int8_down (alloc_int8_*_workspace);
+    sort_pairs (alloc_sort_pairs_workspace), dispatch, combine, combine_backward,
+    route_logits_backward;
 plus TimingEvents (HIP events for layer_profiled) and alloc_workspace.
 Tensors must be CUDA tensors, contiguous, with the dtypes documented in the header.
 """
@@ -115,6 +118,27 @@ EXPORTS = {
     "coli_moe_mxfp4_down": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p, C.c_void_p,
                                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                       C.c_size_t, C.c_void_p]),
+    "coli_moe_int8_quantize": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "coli_moe_int8_linear_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32]),
+    "coli_moe_int8_linear": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                       C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "coli_moe_int8_experts_workspace_bytes": (C.c_size_t, [C.c_void_p, C.c_int32]),
+    "coli_moe_int8_gate_up": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "coli_moe_int8_down": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p, C.c_void_p,
+                                     C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                     C.c_size_t, C.c_void_p]),
+    "coli_moe_sort_pairs_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int32]),
+    "coli_moe_sort_pairs": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "coli_moe_dispatch": (C.c_int, [C.c_void_p, C.c_int, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_int64,
+                                    C.c_void_p, C.c_void_p]),
+    "coli_moe_combine": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "coli_moe_combine_backward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_int32,
+                                            C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "coli_moe_route_logits_backward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int32, C.c_void_p, C.c_void_p,
+                                                 C.c_void_p, C.c_void_p]),
     "coli_moe_num_stages": (C.c_int, []),
     "coli_moe_stage_name": (C.c_char_p, [C.c_int32]),
     "coli_moe_strerror": (C.c_char_p, [C.c_int]),
@@ -454,12 +478,17 @@ def make_router(n_experts, top_k, n_group=1, topk_group=1, score="sigmoid", grou
 _ELEM = {}
 
 
-def _elem(t, name) -> int:
-    """coli_dtype of a tensor."""
+def _elem_init():
     if not _ELEM:
         import torch
-        _ELEM.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, "u8": torch.uint8, "i32": torch.int32,
-                      "f32": torch.float32, "stream": torch._C._cuda_getCurrentRawStream, "dev": torch._C._cuda_getDevice})
+        _ELEM.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, "u8": torch.uint8, "i8": torch.int8,
+                      "i32": torch.int32, "f32": torch.float32, "stream": torch._C._cuda_getCurrentRawStream,
+                      "dev": torch._C._cuda_getDevice})
+
+
+def _elem(t, name) -> int:
+    """coli_dtype of a tensor."""
+    _elem_init()
     d = _ELEM.get(t.dtype)
     if d is None:
         raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
@@ -580,3 +609,134 @@ def mxfp4_down(cfg: Cfg, w: Weights, h, topk_idx, topk_w, off, perm, active, n_a
          _arg(topk_idx, _ELEM["i32"], (T, k), dev, "topk_idx"), _arg(topk_w, _ELEM["f32"], (T, k), dev, "topk_w"),
          *_grouping(cfg, T, off, perm, active, n_active, dev), _arg(out, dt, (T, cfg.hidden), dev, "out"),
          _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
+
+
+# ------------------------------------------------------------------ int8 with token and channel scales
+def int8_quantize(x, codes, scales, stream=None):
+    """coli_moe_int8_quantize: x [rows][cols] -> codes int8 [rows][cols], scales fp32 [rows]."""
+    rows, cols = x.shape
+    d, dev = _elem(x, "x"), x.get_device()
+    _run("coli_moe_int8_quantize", dev, stream, _arg(x, x.dtype, None, dev, "x"), d, rows, cols,
+         _arg(codes, _ELEM["i8"], (rows, cols), dev, "codes"), _arg(scales, _ELEM["f32"], (rows,), dev, "scales"))
+
+
+def alloc_int8_linear_workspace(M_max: int, N: int, K: int, device="cuda"):
+    return _workspace("coli_moe_int8_linear_workspace_bytes", M_max, N, K)(device)
+
+
+def int8_linear(x, codes, scales, out, workspace, bias=None, stream=None):
+    """coli_moe_int8_linear: out [M][N] = int8(x [M][K]) W^T + bias, W = codes int8 [N][K] with scales fp32 [N]."""
+    M, K = x.shape
+    N = codes.shape[0]
+    dt, dev = x.dtype, x.get_device()
+    d = _elem(x, "x")
+    f32 = _ELEM["f32"]
+    _run("coli_moe_int8_linear", dev, stream, _arg(x, dt, None, dev, "x"), d, _arg(codes, _ELEM["i8"], (N, K), dev, "codes"),
+         _arg(scales, f32, (N,), dev, "scales"), None if bias is None else _arg(bias, f32, (N,), dev, "bias"), M, N, K,
+         _arg(out, dt, (M, N), dev, "out"), _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
+
+
+def alloc_int8_experts_workspace(cfg: Cfg, T_max: int, device="cuda"):
+    return _workspace("coli_moe_int8_experts_workspace_bytes", C.byref(cfg), T_max)(device)
+
+
+def _int8_weights(cfg, w, dev):
+    n = cfg.n_experts + cfg.has_shared
+    if w.experts.numel() != n * 3 * cfg.hidden * cfg.ffn or w.scales.numel() != n * (2 * cfg.ffn + cfg.hidden):
+        raise ValueError("weights: sizes do not match the configuration")
+    codes = w.experts.dtype if w.experts.dtype in (_ELEM["i8"], _ELEM["u8"]) else _ELEM["i8"]
+    return C.byref(_Weights(_arg(w.experts, codes, None, dev, "experts"), _arg(w.scales, _ELEM["f32"], None, dev, "scales"),
+                            None, None))
+
+
+def int8_gate_up(cfg: Cfg, w: Weights, x, off, perm, active, n_active, h, workspace, stream=None):
+    """coli_moe_int8_gate_up: h [T k + T shared][F] = silu(gate) * up of every pair of the route. The
+    experts (wbits 8) may be int8 or, as coli_moe_ffn takes them, uint8."""
+    T, dt, dev = x.shape[0], x.dtype, x.get_device()
+    d = _elem(x, "x")
+    _run("coli_moe_int8_gate_up", dev, stream, C.byref(cfg), _int8_weights(cfg, w, dev),
+         _arg(x, dt, (T, cfg.hidden), dev, "x"), d, T, *_grouping(cfg, T, off, perm, active, n_active, dev),
+         _arg(h, dt, (T * (cfg.top_k + cfg.has_shared), cfg.ffn), dev, "h"),
+         _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
+
+
+def int8_down(cfg: Cfg, w: Weights, h, topk_idx, topk_w, off, perm, active, n_active, out, workspace, stream=None):
+    """coli_moe_int8_down: out [T][H] = the pairs' down rows, weighted and summed, + the shared expert's."""
+    T, dt, dev, k = topk_idx.shape[0], h.dtype, h.get_device(), cfg.top_k
+    d = _elem(h, "h")
+    _run("coli_moe_int8_down", dev, stream, C.byref(cfg), _int8_weights(cfg, w, dev),
+         _arg(h, dt, (T * (k + cfg.has_shared), cfg.ffn), dev, "h"), d, T,
+         _arg(topk_idx, _ELEM["i32"], (T, k), dev, "topk_idx"), _arg(topk_w, _ELEM["f32"], (T, k), dev, "topk_w"),
+         *_grouping(cfg, T, off, perm, active, n_active, dev), _arg(out, dt, (T, cfg.hidden), dev, "out"),
+         _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
+
+
+# ------------------------------------------------------------------ pairs to their experts and back
+def alloc_sort_pairs_workspace(pairs_max: int, n_experts: int, device="cuda"):
+    return _workspace("coli_moe_sort_pairs_workspace_bytes", pairs_max, n_experts)(device)
+
+
+def sort_pairs(topk_idx, off, perm, pos, active, n_active, workspace, stream=None):
+    """coli_moe_sort_pairs: topk_idx [T][k] -> off [E + 1], perm, pos [T k], active [E], n_active [1], all int32."""
+    _elem_init()
+    T, k = topk_idx.shape
+    dev, i32, E = topk_idx.get_device(), _ELEM["i32"], active.shape[0]
+    _run("coli_moe_sort_pairs", dev, stream, _arg(topk_idx, i32, None, dev, "topk_idx"), T, k, E,
+         _arg(off, i32, (E + 1,), dev, "off"), _arg(perm, i32, (T * k,), dev, "perm"), _arg(pos, i32, (T * k,), dev, "pos"),
+         _arg(active, i32, (E,), dev, "active"), _arg(n_active, i32, (1,), dev, "n_active"),
+         _arg(workspace, _ELEM["u8"], None, dev, "workspace"), workspace.numel())
+
+
+def _slots(pos, T, what):
+    k = pos.numel() // T if T else 1
+    if k * T != pos.numel() or (T and k == 0):
+        raise ValueError(f"pos: expected the places of {what}'s {T} rows' pairs, got {pos.numel()}")
+    return k
+
+
+def dispatch(x, pos, rows, stream=None):
+    """coli_moe_dispatch: x [T][H] -> rows [R][H], row pos[t k + j] = x row t. pos int32 [T k]."""
+    T, H = x.shape
+    d, dev = _elem(x, "x"), x.get_device()
+    k = _slots(pos, T, "x")
+    _run("coli_moe_dispatch", dev, stream, _arg(x, x.dtype, None, dev, "x"), d, T, k, H,
+         _arg(pos, _ELEM["i32"], None, dev, "pos"), rows.shape[0], _arg(rows, x.dtype, (rows.shape[0], H), dev, "rows"))
+
+
+def combine(rows, pos, out, topk_w=None, add=None, stream=None):
+    """coli_moe_combine: out [T][H] = sum_j topk_w[t][j] rows[pos[t k + j]] + add[t]; without topk_w
+    the gradient of dispatch."""
+    T, H = out.shape
+    dt, dev = out.dtype, out.get_device()
+    d = _elem(out, "out")
+    k = _slots(pos, T, "out")
+    _run("coli_moe_combine", dev, stream, _arg(rows, dt, (rows.shape[0], H), dev, "rows"), d, rows.shape[0], T, k, H,
+         _arg(pos, _ELEM["i32"], None, dev, "pos"),
+         None if topk_w is None else _arg(topk_w, _ELEM["f32"], (T, k), dev, "topk_w"),
+         None if add is None else _arg(add, dt, (T, H), dev, "add"), _arg(out, dt, None, dev, "out"))
+
+
+def combine_backward(dout, rows, pos, topk_w, drows=None, dtopk_w=None, stream=None):
+    """coli_moe_combine_backward: the gradients of combine's rows (drows [R][H]) and weights (dtopk_w
+    fp32 [T][k]); either may be None. rows: combine's, None without dtopk_w."""
+    T, H = dout.shape
+    dt, dev = dout.dtype, dout.get_device()
+    d = _elem(dout, "dout")
+    k = _slots(pos, T, "dout")
+    f32 = _ELEM["f32"]
+    some = drows if rows is None else rows
+    R = 0 if some is None else some.shape[0]
+    _run("coli_moe_combine_backward", dev, stream, _arg(dout, dt, None, dev, "dout"),
+         None if rows is None else _arg(rows, dt, (R, H), dev, "rows"), d, R, T, k, H,
+         _arg(pos, _ELEM["i32"], None, dev, "pos"), _arg(topk_w, f32, (T, k), dev, "topk_w"),
+         None if drows is None else _arg(drows, dt, (R, H), dev, "drows"),
+         None if dtopk_w is None else _arg(dtopk_w, f32, (T, k), dev, "dtopk_w"))
+
+
+def route_logits_backward(router: Router, logits, topk_idx, dtopk_w, dlogits, stream=None):
+    """coli_moe_route_logits_backward: dlogits [T][E] from the gradient dtopk_w fp32 [T][k] of route_logits' weights."""
+    d, dev = _elem(logits, "logits"), logits.get_device()
+    T, E, k = logits.shape[0], router.n_experts, router.top_k
+    _run("coli_moe_route_logits_backward", dev, stream, C.byref(router),
+         _arg(logits, logits.dtype, (T, E), dev, "logits"), d, T, _arg(topk_idx, _ELEM["i32"], (T, k), dev, "topk_idx"),
+         _arg(dtopk_w, _ELEM["f32"], (T, k), dev, "dtopk_w"), _arg(dlogits, logits.dtype, (T, E), dev, "dlogits"))

@@ -223,6 +223,7 @@ struct RouteLogitsArgs {
   float *w;           // [T][k] out
   int m, lshift, vec; // set by the launcher: E / G, log2 of the lanes of a group, whole aligned lanes
 };
+int check_router(const coli_moe_router *r);
 hipError_t launch_route_logits(const RouteLogitsArgs &a, const void *z, int dtype, hipStream_t s);
 
 // Quantised activations are held with their rows padded to a multiple of the K stage.
@@ -272,6 +273,63 @@ hipError_t launch_mx_tile(MxMode mode, int dtype, const MxArgs &a, hipStream_t s
 int64_t mx_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared);  // most row tiles of a route
 hipError_t launch_mx_combine(const float *y, const int32_t *idx, const float *w, int T, int k, int E, int H,
                              int has_shared, void *out, int dtype, hipStream_t s);
+
+// ---- Products in int8 with token and channel scales (int8_*.hip)
+// Quantised activations are held with their rows padded to a multiple of a K group, the rest zero.
+constexpr int I8_KGROUP = 256;
+__host__ __device__ inline int i8_padded(int K) { return (K + I8_KGROUP - 1) / I8_KGROUP * I8_KGROUP; }
+
+enum I8Mode { I8_LINEAR, I8_GATEUP, I8_DOWN };
+
+struct I8Args {
+  const int8_t *wq;               // weight codes (expert 0)
+  const float *ws;                // channel scales (expert 0)
+  int64_t wq_stride, ws_stride;   // bytes, scales per expert
+  const float *bias;              // linear only (null: none)
+  int32_t N, K;                   // output columns (weight rows of a matrix), inputs
+  const void *x;                  // activations that the kernel quantises itself (null: those below)
+  const int8_t *aq;               // quantised activations, rows of i8_padded(K)
+  const float *as;                // their scales
+  int32_t M;                      // rows (linear); tokens (experts)
+  int32_t E, k, has_shared;       // experts only, as is the grouping below
+  const int32_t *off, *perm, *active, *nact;
+  void *out;                      // linear [M][N], gate/up h [pairs][N], down fp32 [pairs][N]
+};
+
+hipError_t launch_i8_quantize(const void *x, int dtype, int64_t rows, int K, int pitch, int8_t *codes, float *scales,
+                              hipStream_t s);
+hipError_t launch_i8_gemv(I8Mode mode, int dtype, const I8Args &a, hipStream_t s);
+bool i8_gemv_from_x(const I8Args &a);  // launch_i8_gemv with x set takes these sizes
+
+// ---- A route's pairs to their experts and back (pairs.hip), the route's gradient (route_grad.hip)
+struct SortArgs {
+  const int32_t *idx;
+  int32_t P, E, chunk;
+  int32_t *hist;  // workspace [chunks][E + 1]
+  int32_t *off, *perm, *pos, *active, *nact;
+};
+int sort_chunks(int64_t P);       // workgroups, each with a row of counts in the workspace
+int sort_most_chunks(int64_t P);  // the most of any number of pairs up to P
+hipError_t launch_sort_pairs(SortArgs a, hipStream_t s);
+
+struct PairArgs {
+  int32_t T, k, H;
+  const int32_t *pos;
+  const float *w;  // null: 1
+  int64_t rows;
+};
+hipError_t launch_dispatch(const PairArgs &a, int dtype, const void *x, void *xs, hipStream_t s);
+hipError_t launch_pair_combine(const PairArgs &a, int dtype, const void *ys, const void *add, void *out, hipStream_t s);
+hipError_t launch_pair_grad(const PairArgs &a, int dtype, const void *dout, const void *ys, void *dys, float *dw,
+                            hipStream_t s);
+
+struct RouteGradArgs {
+  int32_t T, E, k, softmax, renorm;
+  float scale;
+  const int32_t *idx;
+  const float *dw;
+};
+hipError_t launch_route_grad(const RouteGradArgs &a, const void *z, int dtype, void *dz, hipStream_t s);
 
 hipError_t launch_combine(const float *ypair, const float *w, int32_t T, int32_t k, int32_t H,
                           int32_t has_shared, float *out, hipStream_t s);

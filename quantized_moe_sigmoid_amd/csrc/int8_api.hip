@@ -1,0 +1,293 @@
+// int8_api.hip — the C entry points of the int8 products with token and channel scales, of the
+// pairs' way to their experts and back, and of the route's gradient: host-side validation, workspace
+// layout, launches (one stream, no host synchronisation, no device allocation).
+#include "coli_internal.h"
+
+namespace coli {
+
+static bool i8_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+static int i8_dev(hipError_t e) { return e == hipSuccess ? COLI_OK : COLI_E_DEVICE; }
+static bool i8_dtype(int d) { return d == COLI_F32 || d == COLI_BF16 || d == COLI_F16; }
+static size_t i8_elem(int d) { return d == COLI_F32 ? 4 : 2; }
+static size_t i8_al256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+constexpr int32_t I8_MAX_K = 1 << 17;  // 127 * 128 * K < 2^31
+
+// A workspace: quantised activations (codes, scales), then the down product's fp32 rows.
+struct I8Ws {
+  size_t aq, as, y, total;
+};
+
+static I8Ws i8_ws(int64_t rows, int K, size_t y_bytes) {
+  I8Ws L{};
+  size_t o = 0;
+  L.aq = o;  o = i8_al256(o + (size_t)rows * i8_padded(K));
+  L.as = o;  o = i8_al256(o + (size_t)rows * sizeof(float));
+  L.y = o;   o = i8_al256(o + y_bytes);
+  L.total = o;
+  return L;
+}
+
+static int64_t i8_rows(const coli_moe_cfg &c, int32_t T) { return (int64_t)T * (c.top_k + c.has_shared); }
+static I8Ws i8_ws_gateup(const coli_moe_cfg &c, int32_t T) { return i8_ws(T, c.hidden, 0); }
+static I8Ws i8_ws_down(const coli_moe_cfg &c, int32_t T) {
+  const int64_t R = i8_rows(c, T);
+  return i8_ws(R, c.ffn, (size_t)R * c.hidden * sizeof(float));
+}
+
+static int check_linear(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || N < 0 || K <= 0) return COLI_E_INVALID;
+  if (K % 16 || K > I8_MAX_K || M > (1 << 20) || N > (1 << 20)) return COLI_E_UNSUPPORTED;
+  if ((int64_t)M * K >= ((int64_t)1 << 37) || (int64_t)N * K >= ((int64_t)1 << 37)) return COLI_E_UNSUPPORTED;
+  return COLI_OK;
+}
+
+static int check_experts(const coli_moe_cfg *cfg, const coli_moe_weights *w, int dtype, int32_t T) {
+  int st;
+  if ((st = check_cfg(cfg))) return st;
+  if (cfg->wfmt != COLI_W_INT8 || cfg->scale_group != 0 || !i8_dtype(dtype)) return COLI_E_INVALID;
+  if ((st = check_T(cfg, T))) return st;
+  return T == 0 ? COLI_OK : check_weights(w, true, false);
+}
+
+static I8Args expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int32_t T, const int32_t *off,
+                          const int32_t *perm, const int32_t *active, const int32_t *nact) {
+  I8Args a{};
+  a.wq = static_cast<const int8_t *>(w.experts);
+  a.ws = w.scales;
+  a.wq_stride = (int64_t)coli_moe_blob_bytes(&c);
+  a.ws_stride = (int64_t)coli_moe_scales_per_expert(&c);
+  a.M = T;
+  a.E = c.n_experts;
+  a.k = c.top_k;
+  a.has_shared = c.has_shared;
+  a.off = off;
+  a.perm = perm;
+  a.active = active;
+  a.nact = nact;
+  return a;
+}
+
+static int check_pairs(int dtype, int32_t T, int32_t k, int32_t H, int64_t rows) {
+  if (!i8_dtype(dtype) || T < 0 || k <= 0 || H <= 0 || rows < 0) return COLI_E_INVALID;
+  if ((int64_t)T * k >= (1 << 30) || (int64_t)T * H >= ((int64_t)1 << 40) || rows >= ((int64_t)1 << 40) / H)
+    return COLI_E_UNSUPPORTED;
+  return COLI_OK;
+}
+
+}  // namespace coli
+
+using namespace coli;
+
+extern "C" {
+
+int coli_moe_int8_quantize(const void *x, int dtype, int64_t rows, int32_t cols, int8_t *codes, float *scales,
+                           void *stream) {
+  if (rows < 0 || cols <= 0 || !i8_dtype(dtype)) return COLI_E_INVALID;
+  if (cols % 16 || cols > I8_MAX_K || rows >= ((int64_t)1 << 31) || rows >= ((int64_t)1 << 40) / cols)
+    return COLI_E_UNSUPPORTED;
+  if (rows == 0) return COLI_OK;
+  if (!x || !codes || !scales) return COLI_E_INVALID;
+  if (!i8_aligned(x, 16) || !i8_aligned(codes, 16) || !i8_aligned(scales, 4)) return COLI_E_ALIGN;
+  return i8_dev(launch_i8_quantize(x, dtype, rows, cols, cols, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+size_t coli_moe_int8_linear_workspace_bytes(int32_t M_max, int32_t N, int32_t K) {
+  if (check_linear(M_max, N, K) != COLI_OK) return 0;
+  return i8_ws(M_max > 0 ? M_max : 1, K, 0).total;
+}
+
+int coli_moe_int8_linear(const void *x, int dtype, const int8_t *codes, const float *scales, const float *bias, int32_t M,
+                         int32_t N, int32_t K, void *y, void *workspace, size_t ws_bytes, void *stream) {
+  int st;
+  if (!i8_dtype(dtype)) return COLI_E_INVALID;
+  if ((st = check_linear(M, N, K))) return st;
+  if (M == 0 || N == 0) return COLI_OK;
+  if (!x || !codes || !scales || !y) return COLI_E_INVALID;
+  if (!i8_aligned(x, 16) || !i8_aligned(codes, 16) || !i8_aligned(y, 16) || !i8_aligned(scales, 4) || !i8_aligned(bias, 4))
+    return COLI_E_ALIGN;
+  const I8Ws L = i8_ws(M, K, 0);
+  if (!workspace || ws_bytes < L.total) return COLI_E_WORKSPACE;
+  if (!i8_aligned(workspace, 256)) return COLI_E_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  I8Args a{};
+  a.wq = codes;
+  a.ws = scales;
+  a.bias = bias;
+  a.N = N;
+  a.K = K;
+  a.M = M;
+  a.out = y;
+  int8_t *aq = reinterpret_cast<int8_t *>(ws + L.aq);
+  float *as = reinterpret_cast<float *>(ws + L.as);
+  if (i8_gemv_from_x(a))
+    a.x = x;
+  else if ((st = i8_dev(launch_i8_quantize(x, dtype, M, K, i8_padded(K), aq, as, s))))
+    return st;
+  a.aq = aq;
+  a.as = as;
+  return i8_dev(launch_i8_gemv(I8_LINEAR, dtype, a, s));
+}
+
+size_t coli_moe_int8_experts_workspace_bytes(const coli_moe_cfg *cfg, int32_t T_max) {
+  if (check_cfg(cfg) != COLI_OK || cfg->wfmt != COLI_W_INT8 || cfg->scale_group != 0 || check_T(cfg, T_max) != COLI_OK)
+    return 0;
+  const int32_t T = T_max > 0 ? T_max : 1;
+  const size_t g = i8_ws_gateup(*cfg, T).total, d = i8_ws_down(*cfg, T).total;
+  return g > d ? g : d;
+}
+
+int coli_moe_int8_gate_up(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *x, int dtype, int32_t T,
+                          const int32_t *expert_off, const int32_t *pair_perm, const int32_t *active,
+                          const int32_t *n_active, void *h, void *workspace, size_t ws_bytes, void *stream) {
+  int st;
+  if ((st = check_experts(cfg, w, dtype, T))) return st;
+  if (T == 0) return COLI_OK;
+  if (!x || !expert_off || !pair_perm || !active || !n_active || !h) return COLI_E_INVALID;
+  if (!i8_aligned(x, 16) || !i8_aligned(h, 16) || !i8_aligned(expert_off, 4) || !i8_aligned(pair_perm, 4) ||
+      !i8_aligned(active, 4) || !i8_aligned(n_active, 4))
+    return COLI_E_ALIGN;
+  const I8Ws L = i8_ws_gateup(*cfg, T);
+  if (!workspace || ws_bytes < L.total) return COLI_E_WORKSPACE;
+  if (!i8_aligned(workspace, 256)) return COLI_E_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  I8Args a = expert_args(*cfg, *w, T, expert_off, pair_perm, active, n_active);
+  a.N = cfg->ffn;
+  a.K = cfg->hidden;
+  int8_t *aq = reinterpret_cast<int8_t *>(ws + L.aq);
+  float *as = reinterpret_cast<float *>(ws + L.as);
+  if (i8_gemv_from_x(a))
+    a.x = x;
+  else if ((st = i8_dev(launch_i8_quantize(x, dtype, T, cfg->hidden, i8_padded(cfg->hidden), aq, as, s))))
+    return st;
+  a.aq = aq;
+  a.as = as;
+  a.out = h;
+  return i8_dev(launch_i8_gemv(I8_GATEUP, dtype, a, s));
+}
+
+int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *h, int dtype, int32_t T,
+                       const int32_t *topk_idx, const float *topk_w, const int32_t *expert_off,
+                       const int32_t *pair_perm, const int32_t *active, const int32_t *n_active, void *out,
+                       void *workspace, size_t ws_bytes, void *stream) {
+  int st;
+  if ((st = check_experts(cfg, w, dtype, T))) return st;
+  if (T == 0) return COLI_OK;
+  if (!h || !topk_idx || !topk_w || !expert_off || !pair_perm || !active || !n_active || !out) return COLI_E_INVALID;
+  if (!i8_aligned(h, 16) || !i8_aligned(out, 16) || !i8_aligned(topk_idx, 4) || !i8_aligned(topk_w, 4) ||
+      !i8_aligned(expert_off, 4) || !i8_aligned(pair_perm, 4) || !i8_aligned(active, 4) || !i8_aligned(n_active, 4))
+    return COLI_E_ALIGN;
+  const I8Ws L = i8_ws_down(*cfg, T);
+  if (!workspace || ws_bytes < L.total) return COLI_E_WORKSPACE;
+  if (!i8_aligned(workspace, 256)) return COLI_E_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  I8Args a = expert_args(*cfg, *w, T, expert_off, pair_perm, active, n_active);
+  a.wq += 2 * (int64_t)cfg->ffn * cfg->hidden;  // gate and up rows
+  a.ws += 2 * (int64_t)cfg->ffn;
+  a.N = cfg->hidden;
+  a.K = cfg->ffn;
+  int8_t *aq = reinterpret_cast<int8_t *>(ws + L.aq);
+  float *as = reinterpret_cast<float *>(ws + L.as), *y = reinterpret_cast<float *>(ws + L.y);
+  if ((st = i8_dev(launch_i8_quantize(h, dtype, i8_rows(*cfg, T), cfg->ffn, i8_padded(cfg->ffn), aq, as, s)))) return st;
+  a.aq = aq;
+  a.as = as;
+  a.out = y;
+  if ((st = i8_dev(launch_i8_gemv(I8_DOWN, dtype, a, s)))) return st;
+  return i8_dev(launch_mx_combine(y, topk_idx, topk_w, T, cfg->top_k, cfg->n_experts, cfg->hidden, cfg->has_shared, out,
+                                  dtype, s));
+}
+
+size_t coli_moe_sort_pairs_workspace_bytes(int64_t P, int32_t n_experts) {
+  if (P < 0 || P >= (1 << 30) || n_experts <= 0 || n_experts > 1024) return 0;
+  // fewer pairs may be cut into more chunks than P of them, up to the most chunks there are
+  return i8_al256((size_t)sort_most_chunks(P) * (n_experts + 1) * sizeof(int32_t));
+}
+
+int coli_moe_sort_pairs(const int32_t *topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t *expert_off,
+                        int32_t *pair_perm, int32_t *pair_pos, int32_t *active, int32_t *n_active, void *workspace,
+                        size_t ws_bytes, void *stream) {
+  if (T < 0 || k <= 0 || n_experts <= 0) return COLI_E_INVALID;
+  const int64_t P = (int64_t)T * k;
+  if (P >= (1 << 30) || n_experts > 1024) return COLI_E_UNSUPPORTED;
+  if (T == 0) return COLI_OK;
+  if (!topk_idx || !expert_off || !pair_perm || !pair_pos || !active || !n_active) return COLI_E_INVALID;
+  if (!i8_aligned(topk_idx, 4) || !i8_aligned(expert_off, 4) || !i8_aligned(pair_perm, 4) || !i8_aligned(pair_pos, 4) ||
+      !i8_aligned(active, 4) || !i8_aligned(n_active, 4))
+    return COLI_E_ALIGN;
+  if (!workspace || ws_bytes < (size_t)sort_chunks(P) * (n_experts + 1) * sizeof(int32_t)) return COLI_E_WORKSPACE;
+  if (!i8_aligned(workspace, 256)) return COLI_E_ALIGN;
+  SortArgs a{};
+  a.idx = topk_idx;
+  a.P = (int32_t)P;
+  a.E = n_experts;
+  a.hist = static_cast<int32_t *>(workspace);
+  a.off = expert_off;
+  a.perm = pair_perm;
+  a.pos = pair_pos;
+  a.active = active;
+  a.nact = n_active;
+  return i8_dev(launch_sort_pairs(a, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_dispatch(const void *x, int dtype, int32_t T, int32_t k, int32_t H, const int32_t *pair_pos, int64_t rows,
+                      void *xs, void *stream) {
+  const int st = check_pairs(dtype, T, k, H, rows);
+  if (st || T == 0 || rows == 0) return st;
+  if (!x || !pair_pos || !xs) return COLI_E_INVALID;
+  const size_t e = i8_elem(dtype);
+  if (!i8_aligned(x, e) || !i8_aligned(xs, e) || !i8_aligned(pair_pos, 4)) return COLI_E_ALIGN;
+  const PairArgs a{T, k, H, pair_pos, nullptr, rows};
+  return i8_dev(launch_dispatch(a, dtype, x, xs, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_combine(const void *ys, int dtype, int64_t rows, int32_t T, int32_t k, int32_t H, const int32_t *pair_pos,
+                     const float *topk_w, const void *add, void *out, void *stream) {
+  const int st = check_pairs(dtype, T, k, H, rows);
+  if (st || T == 0) return st;
+  if ((!ys && rows > 0) || !pair_pos || !out) return COLI_E_INVALID;
+  const size_t e = i8_elem(dtype);
+  if (!i8_aligned(ys, e) || !i8_aligned(add, e) || !i8_aligned(out, e) || !i8_aligned(pair_pos, 4) || !i8_aligned(topk_w, 4))
+    return COLI_E_ALIGN;
+  const PairArgs a{T, k, H, pair_pos, topk_w, rows};
+  return i8_dev(launch_pair_combine(a, dtype, ys, add, out, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_combine_backward(const void *dout, const void *ys, int dtype, int64_t rows, int32_t T, int32_t k, int32_t H,
+                              const int32_t *pair_pos, const float *topk_w, void *dys, float *dtopk_w, void *stream) {
+  const int st = check_pairs(dtype, T, k, H, rows);
+  if (st || T == 0) return st;
+  if (!dout || !pair_pos || !topk_w || (!dys && !dtopk_w) || (dtopk_w && !ys && rows > 0)) return COLI_E_INVALID;
+  const size_t e = i8_elem(dtype);
+  if (!i8_aligned(dout, e) || !i8_aligned(ys, e) || !i8_aligned(dys, e) || !i8_aligned(pair_pos, 4) ||
+      !i8_aligned(topk_w, 4) || !i8_aligned(dtopk_w, 4))
+    return COLI_E_ALIGN;
+  const PairArgs a{T, k, H, pair_pos, topk_w, rows};
+  return i8_dev(launch_pair_grad(a, dtype, dout, ys, dys, dtopk_w, static_cast<hipStream_t>(stream)));
+}
+
+int coli_moe_route_logits_backward(const coli_moe_router *r, const void *z, int dtype, int32_t T, const int32_t *topk_idx,
+                                   const float *dtopk_w, void *dz, void *stream) {
+  int st;
+  if (!i8_dtype(dtype) || T < 0) return COLI_E_INVALID;
+  if ((st = check_router(r))) return st;
+  if (T > (1 << 26) - 4) return COLI_E_UNSUPPORTED;  // 64 threads a token, fewer than 2^32
+  if (T == 0) return COLI_OK;
+  if (!z || !topk_idx || !dtopk_w || !dz) return COLI_E_INVALID;
+  const size_t e = i8_elem(dtype);
+  if (!i8_aligned(z, e) || !i8_aligned(dz, e) || !i8_aligned(topk_idx, 4) || !i8_aligned(dtopk_w, 4)) return COLI_E_ALIGN;
+  RouteGradArgs a{};
+  a.T = T;
+  a.E = r->n_experts;
+  a.k = r->top_k;
+  a.softmax = r->score == COLI_SCORE_SOFTMAX;
+  a.renorm = r->renorm;
+  a.scale = r->scale;
+  a.idx = topk_idx;
+  a.dw = dtopk_w;
+  return i8_dev(launch_route_grad(a, z, dtype, dz, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

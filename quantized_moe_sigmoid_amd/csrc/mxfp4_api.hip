@@ -105,6 +105,18 @@ static hipError_t launch_experts(MxMode mode, int dtype, MxArgs &a, uint8_t *ws,
   return launch_mx_tile(mode, dtype, a, s);
 }
 
+int check_router(const coli_moe_router *r) {
+  if (!r) return COLI_E_INVALID;
+  if (r->n_experts <= 0 || r->top_k <= 0 || r->n_group <= 0 || r->topk_group <= 0) return COLI_E_INVALID;
+  if (r->n_experts % r->n_group || r->topk_group > r->n_group) return COLI_E_INVALID;
+  if (r->top_k > r->topk_group * (r->n_experts / r->n_group)) return COLI_E_INVALID;
+  if ((r->group_top != 1 && r->group_top != 2) || (r->renorm != 0 && r->renorm != 1)) return COLI_E_INVALID;
+  if (r->score != COLI_SCORE_SIGMOID && r->score != COLI_SCORE_SOFTMAX) return COLI_E_INVALID;
+  if (!(r->scale == r->scale)) return COLI_E_INVALID;  // NaN
+  if (r->n_experts > 1024 || r->n_group > 64 || r->top_k > 64) return COLI_E_UNSUPPORTED;
+  return COLI_OK;
+}
+
 }  // namespace coli
 
 using namespace coli;
@@ -113,14 +125,9 @@ extern "C" {
 
 int coli_moe_route_logits(const coli_moe_router *r, const void *z, int dtype, int32_t T, const float *bias,
                           int32_t *topk_idx, float *topk_w, void *stream) {
-  if (!r || !mx_dtype(dtype) || T < 0) return COLI_E_INVALID;
-  if (r->n_experts <= 0 || r->top_k <= 0 || r->n_group <= 0 || r->topk_group <= 0) return COLI_E_INVALID;
-  if (r->n_experts % r->n_group || r->topk_group > r->n_group) return COLI_E_INVALID;
-  if (r->top_k > r->topk_group * (r->n_experts / r->n_group)) return COLI_E_INVALID;
-  if ((r->group_top != 1 && r->group_top != 2) || (r->renorm != 0 && r->renorm != 1)) return COLI_E_INVALID;
-  if (r->score != COLI_SCORE_SIGMOID && r->score != COLI_SCORE_SOFTMAX) return COLI_E_INVALID;
-  if (!(r->scale == r->scale)) return COLI_E_INVALID;  // NaN
-  if (r->n_experts > 1024 || r->n_group > 64 || r->top_k > 64) return COLI_E_UNSUPPORTED;
+  int st;
+  if (!mx_dtype(dtype) || T < 0) return COLI_E_INVALID;
+  if ((st = check_router(r))) return st;
   if (T > (1 << 26) - 4) return COLI_E_UNSUPPORTED;  // 64 threads a token, fewer than 2^32
   if (T == 0) return COLI_OK;
   if (!z || !topk_idx || !topk_w) return COLI_E_INVALID;

@@ -1,0 +1,131 @@
+// route_grad.hip — the gradient of the route from logits (route_logits.hip; colibri-strix README,
+// "What's implemented", router item) with respect to the logits.
+//
+// The taken experts are held fixed, so a weight depends on the taken scores alone (sigmoid, or any
+// score over its sum) or on all logits (softmax). With p the scores, S their sum over the taken and
+// g the weights' gradient:
+//   renorm: scale (g_j - sum_i g_i p_i / S) p_j / S, times 1 - p_j for the sigmoid;
+//   else scale g_j p_j (1 - p_j), or p_e scale (g_e - sum_i g_i p_i) for every expert.
+// All of it in fp64: what is left of g_j is a difference. A single taken expert has p / S = 1 and so
+// exactly 0.
+//
+// One wavefront a token: its logits in registers, the slots in the first k lanes and handed to all
+// by scalar reads, so that an expert in two slots gets their sum in slot order.
+#include "mxfp4_impl.h"
+
+namespace coli {
+
+constexpr int RG_WAVES = 4;
+
+__device__ __forceinline__ double wave_total(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// z and dz may be one array: a wavefront has read its row before it writes it
+template <int EPL, bool SOFTMAX, typename T>
+__global__ __launch_bounds__(64 * RG_WAVES) void route_grad_kernel(RouteGradArgs a, const T *z, T *dz) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * RG_WAVES + (threadIdx.x >> 6);
+  if (t >= a.T) return;
+  const int E = a.E, k = a.k;
+  const T *zt = z + t * E;
+  float v[EPL];  // -inf: not there
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < EPL; i++) {
+    const int e = lane + 64 * i;
+    const float x = e < E ? (float)zt[e] : -INFINITY;
+    v[i] = x == x ? x : -INFINITY;
+    top = fmaxf(top, v[i]);
+  }
+  int mine = lane < k ? a.idx[t * k + lane] : -1;
+  if (mine >= E) mine = -1;
+  float zs = mine >= 0 ? (float)zt[mine] : -INFINITY;
+  if (!(zs > -INFINITY)) zs = -INFINITY;
+  const double g = lane < k && mine >= 0 ? (double)a.dw[t * k + lane] : 0.0;
+  double p[SOFTMAX ? EPL : 1], ps, rest = 1.0;  // scores; of this lane's slot; 1 - p of a sigmoid
+  if constexpr (SOFTMAX) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    // logits of +inf share everything and move nothing
+    const bool some = top > -INFINITY && top < INFINITY;
+    ps = some && zs > -INFINITY ? exp((double)zs - (double)top) : 0.0;
+    if (!a.renorm) {
+      double total = 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; i++) {
+        p[i] = some && v[i] > -INFINITY ? exp((double)v[i] - (double)top) : 0.0;
+        total += p[i];
+      }
+      total = wave_total(total);
+      const double inv = total > 0.0 ? 1.0 / total : 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; i++) p[i] *= inv;
+      ps *= inv;
+    }
+  } else {
+    const double x = exp(-fabs((double)zs));
+    ps = zs > -INFINITY ? (zs >= 0.0f ? 1.0 : x) / (1.0 + x) : 0.0;
+    rest = (zs >= 0.0f ? x : 1.0) / (1.0 + x);
+  }
+  // what this lane's slot gives its expert
+  double mean = 0.0, give;
+  if (a.renorm) {
+    const double total = wave_total(ps);
+    const double share = total > 0.0 ? ps / total : 0.0;
+    mean = wave_total(share > 0.0 ? g * share : 0.0);
+    give = share > 0.0 ? (double)a.scale * (g - mean) * share * rest : 0.0;
+  } else if constexpr (SOFTMAX) {
+    mean = wave_total(ps > 0.0 ? g * ps : 0.0) * (double)a.scale;
+    give = g * (double)a.scale;
+  } else {
+    give = ps > 0.0 ? (double)a.scale * g * ps * rest : 0.0;
+  }
+  double out[EPL] = {};
+  for (int j = 0; j < k; j++) {
+    const int e = __builtin_amdgcn_readlane(mine, j);
+    if (e < 0) continue;
+    const double add = lane_value(give, j);
+#pragma unroll
+    for (int i = 0; i < EPL; i++) out[i] += e == lane + 64 * i ? add : 0.0;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; i++) {
+    const int e = lane + 64 * i;
+    if (SOFTMAX && !a.renorm) out[i] = p[i] > 0.0 ? p[i] * (out[i] - mean) : 0.0;
+    if (e < E) dz[t * E + e] = (T)out[i];
+  }
+}
+
+template <typename T>
+static hipError_t launch_rg(const RouteGradArgs &a, const T *z, T *dz, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T + RG_WAVES - 1) / RG_WAVES)), block(64 * RG_WAVES);
+  auto go = [&]<int EPL>() {
+    if (a.softmax)
+      hipLaunchKernelGGL((route_grad_kernel<EPL, true, T>), grid, block, 0, s, a, z, dz);
+    else
+      hipLaunchKernelGGL((route_grad_kernel<EPL, false, T>), grid, block, 0, s, a, z, dz);
+    return hipGetLastError();
+  };
+  if (a.E <= 64) return go.template operator()<1>();
+  if (a.E <= 128) return go.template operator()<2>();
+  if (a.E <= 256) return go.template operator()<4>();
+  if (a.E <= 512) return go.template operator()<8>();
+  return go.template operator()<16>();
+}
+
+hipError_t launch_route_grad(const RouteGradArgs &a, const void *z, int dtype, void *dz, hipStream_t s) {
+  if (dtype == COLI_F32) return launch_rg(a, (const float *)z, (float *)dz, s);
+  if (dtype == COLI_BF16) return launch_rg(a, (const bf16_t *)z, (bf16_t *)dz, s);
+  return launch_rg(a, (const f16_t *)z, (f16_t *)dz, s);
+}
+
+}  // namespace coli

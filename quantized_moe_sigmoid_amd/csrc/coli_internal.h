@@ -293,6 +293,9 @@ struct I8Args {
   int32_t M;                      // rows (linear); tokens (experts)
   int32_t E, k, has_shared;       // experts only, as is the grouping below
   const int32_t *off, *perm, *active, *nact;
+  int4 *tiles;                    // row tiles of the route (tiled experts only) and their number
+  int32_t *ntiles;
+  int32_t strip;                  // column tiles that a workgroup runs one after another
   void *out;                      // linear [M][N], gate/up h [pairs][N], down fp32 [pairs][N]
 };
 
@@ -300,6 +303,8 @@ hipError_t launch_i8_quantize(const void *x, int dtype, int64_t rows, int K, int
                               hipStream_t s);
 hipError_t launch_i8_gemv(I8Mode mode, int dtype, const I8Args &a, hipStream_t s);
 bool i8_gemv_from_x(const I8Args &a);  // launch_i8_gemv with x set takes these sizes
+hipError_t launch_i8_tile(I8Mode mode, int dtype, const I8Args &a, hipStream_t s);
+int64_t i8_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared);  // most row tiles of a route
 
 // ---- A route's pairs to their experts and back (pairs.hip), the route's gradient (route_grad.hip)
 struct SortArgs {

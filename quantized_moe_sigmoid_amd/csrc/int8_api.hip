@@ -1,6 +1,8 @@
 // int8_api.hip — the C entry points of the int8 products with token and channel scales, of the
 // pairs' way to their experts and back, and of the route's gradient: host-side validation, workspace
 // layout, launches (one stream, no host synchronisation, no device allocation).
+#include <algorithm>
+
 #include "coli_internal.h"
 
 namespace coli {
@@ -13,26 +15,30 @@ static size_t i8_al256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 constexpr int32_t I8_MAX_K = 1 << 17;  // 127 * 128 * K < 2^31
 
-// A workspace: quantised activations (codes, scales), then the down product's fp32 rows.
+// A workspace: quantised activations (codes, scales), the row tiles of a route, then the down product's
+// fp32 rows.
 struct I8Ws {
-  size_t aq, as, y, total;
+  size_t aq, as, tiles, ntiles, y, total;
 };
 
-static I8Ws i8_ws(int64_t rows, int K, size_t y_bytes) {
+static I8Ws i8_ws(int64_t rows, int K, int64_t tiles, size_t y_bytes) {
   I8Ws L{};
   size_t o = 0;
-  L.aq = o;  o = i8_al256(o + (size_t)rows * i8_padded(K));
-  L.as = o;  o = i8_al256(o + (size_t)rows * sizeof(float));
-  L.y = o;   o = i8_al256(o + y_bytes);
+  L.aq = o;      o = i8_al256(o + (size_t)rows * i8_padded(K));
+  L.as = o;      o = i8_al256(o + (size_t)rows * sizeof(float));
+  L.tiles = o;   o = i8_al256(o + tiles * sizeof(int4));
+  L.ntiles = o;  o = i8_al256(o + (tiles ? sizeof(int32_t) : 0));
+  L.y = o;       o = i8_al256(o + y_bytes);
   L.total = o;
   return L;
 }
 
 static int64_t i8_rows(const coli_moe_cfg &c, int32_t T) { return (int64_t)T * (c.top_k + c.has_shared); }
-static I8Ws i8_ws_gateup(const coli_moe_cfg &c, int32_t T) { return i8_ws(T, c.hidden, 0); }
+static int64_t i8_tiles(const coli_moe_cfg &c, int32_t T) { return i8_tile_cap(T, c.top_k, c.n_experts, c.has_shared); }
+static I8Ws i8_ws_gateup(const coli_moe_cfg &c, int32_t T) { return i8_ws(T, c.hidden, i8_tiles(c, T), 0); }
 static I8Ws i8_ws_down(const coli_moe_cfg &c, int32_t T) {
   const int64_t R = i8_rows(c, T);
-  return i8_ws(R, c.ffn, (size_t)R * c.hidden * sizeof(float));
+  return i8_ws(R, c.ffn, i8_tiles(c, T), (size_t)R * c.hidden * sizeof(float));
 }
 
 static int check_linear(int32_t M, int32_t N, int32_t K) {
@@ -68,6 +74,23 @@ static I8Args expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
   return a;
 }
 
+// A dense product on the tiled kernel?
+static bool i8_linear_tiled(int32_t M, int32_t N) {
+  if (M <= 16) return false;
+  return (M <= 32 ? 2 : (M + 63) / 64 * 4) * (int64_t)N > 40960;
+}
+
+static hipError_t launch_experts(I8Mode mode, int dtype, I8Args &a, uint8_t *ws, const I8Ws &L, hipStream_t s) {
+  // The kernel for few rows up to 512 pairs (decode batches), the tiled one past them; its offsets
+  // into the activations and the output have 32 bits.
+  const int64_t rows = (int64_t)a.M * (a.k + a.has_shared), widest = std::max<int64_t>((int64_t)a.N * 4, i8_padded(a.K));
+  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P || rows * widest >= ((int64_t)1 << 32) - 65536)
+    return launch_i8_gemv(mode, dtype, a, s);
+  a.tiles = reinterpret_cast<int4 *>(ws + L.tiles);
+  a.ntiles = reinterpret_cast<int32_t *>(ws + L.ntiles);
+  return launch_i8_tile(mode, dtype, a, s);
+}
+
 static int check_pairs(int dtype, int32_t T, int32_t k, int32_t H, int64_t rows) {
   if (!i8_dtype(dtype) || T < 0 || k <= 0 || H <= 0 || rows < 0) return COLI_E_INVALID;
   if ((int64_t)T * k >= (1 << 30) || (int64_t)T * H >= ((int64_t)1 << 40) || rows >= ((int64_t)1 << 40) / H)
@@ -94,7 +117,7 @@ int coli_moe_int8_quantize(const void *x, int dtype, int64_t rows, int32_t cols,
 
 size_t coli_moe_int8_linear_workspace_bytes(int32_t M_max, int32_t N, int32_t K) {
   if (check_linear(M_max, N, K) != COLI_OK) return 0;
-  return i8_ws(M_max > 0 ? M_max : 1, K, 0).total;
+  return i8_ws(M_max > 0 ? M_max : 1, K, 0, 0).total;
 }
 
 int coli_moe_int8_linear(const void *x, int dtype, const int8_t *codes, const float *scales, const float *bias, int32_t M,
@@ -106,7 +129,7 @@ int coli_moe_int8_linear(const void *x, int dtype, const int8_t *codes, const fl
   if (!x || !codes || !scales || !y) return COLI_E_INVALID;
   if (!i8_aligned(x, 16) || !i8_aligned(codes, 16) || !i8_aligned(y, 16) || !i8_aligned(scales, 4) || !i8_aligned(bias, 4))
     return COLI_E_ALIGN;
-  const I8Ws L = i8_ws(M, K, 0);
+  const I8Ws L = i8_ws(M, K, 0, 0);
   if (!workspace || ws_bytes < L.total) return COLI_E_WORKSPACE;
   if (!i8_aligned(workspace, 256)) return COLI_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -127,7 +150,7 @@ int coli_moe_int8_linear(const void *x, int dtype, const int8_t *codes, const fl
     return st;
   a.aq = aq;
   a.as = as;
-  return i8_dev(launch_i8_gemv(I8_LINEAR, dtype, a, s));
+  return i8_dev(i8_linear_tiled(M, N) ? launch_i8_tile(I8_LINEAR, dtype, a, s) : launch_i8_gemv(I8_LINEAR, dtype, a, s));
 }
 
 size_t coli_moe_int8_experts_workspace_bytes(const coli_moe_cfg *cfg, int32_t T_max) {
@@ -165,7 +188,7 @@ int coli_moe_int8_gate_up(const coli_moe_cfg *cfg, const coli_moe_weights *w, co
   a.aq = aq;
   a.as = as;
   a.out = h;
-  return i8_dev(launch_i8_gemv(I8_GATEUP, dtype, a, s));
+  return i8_dev(launch_experts(I8_GATEUP, dtype, a, ws, L, s));
 }
 
 int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const void *h, int dtype, int32_t T,
@@ -195,7 +218,7 @@ int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const
   a.aq = aq;
   a.as = as;
   a.out = y;
-  if ((st = i8_dev(launch_i8_gemv(I8_DOWN, dtype, a, s)))) return st;
+  if ((st = i8_dev(launch_experts(I8_DOWN, dtype, a, ws, L, s)))) return st;
   return i8_dev(launch_mx_combine(y, topk_idx, topk_w, T, cfg->top_k, cfg->n_experts, cfg->hidden, cfg->has_shared, out,
                                   dtype, s));
 }

@@ -149,7 +149,9 @@ def _linear(q, x, codes, scales, bias=None, M_max=None):
 
 LINEAR = [(1, 1, 16), (1, 16, 64), (1, 77, 2064), (1, 300, 6144), (1, 5, 49168), (2, 33, 272), (15, 17, 4096), (16, 64, 256),
           (17, 31, 1040), (33, 129, 528), (64, 48, 2048), (65, 130, 4112), (200, 77, 784), (7, 2051, 144), (129, 1, 48),
-          (300, 515, 1008), (513, 1031, 320), (1000, 257, 2064), (257, 256, 16), (770, 520, 112), (512, 512, 8192)]
+          (300, 515, 1008), (513, 1031, 320), (1000, 257, 2064), (257, 256, 16), (770, 520, 112), (512, 512, 8192),
+          (20, 20500, 48), (70, 5200, 272), (300, 2051, 1008), (1000, 1031, 2064), (129, 3460, 16), (513, 4096, 8192), (2900, 4100, 144),
+          (3001, 4361, 400), (3000, 4096, 1024), (257, 49160, 16)]
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -167,7 +169,8 @@ def test_linear_exact(q, dtype, M, N, K):
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("M,N,K", [(1, 300, 2064), (7, 77, 528), (65, 130, 4112), (515, 1027, 272), (300, 768, 1024)])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 2064), (7, 77, 528), (65, 130, 4112), (515, 1027, 272), (300, 768, 1024), (515, 4099, 272),
+                                   (2900, 4352, 528)])
 def test_linear_bias(q, dtype, M, N, K):
     rng = np.random.default_rng(M + N + K)
     x = _rows(rng, M, K, dtype)
@@ -182,11 +185,11 @@ def test_linear_bias(q, dtype, M, N, K):
     assert (np.abs(got - want) <= tol + _half(dtype) * (np.abs(want) + tol) + _tiny(dtype)).all()
 
 
-@pytest.mark.parametrize("M", [1, 3, 40, 300])
+@pytest.mark.parametrize("M", [1, 3, 40, 300, 4100])
 def test_linear_largest_sums(q, M):
     """K = 2^17 with every product at its largest: the sums end just below 2^31."""
     import torch
-    K, N = 131072, 20
+    K, N = 131072, 20 if M < 4000 else 400
     x = torch.full((M, K), 3.0, device="cuda")
     x[:, 1::2] *= -1
     codes = np.full((N, K), -128, np.int8)
@@ -200,13 +203,13 @@ def test_linear_largest_sums(q, M):
     assert np.array_equal(out, np.repeat(want, M, 0))
 
 
-@pytest.mark.parametrize("M", [1, 5, 70, 600])
+@pytest.mark.parametrize("M", [1, 5, 70, 600, 3000])
 def test_linear_rows_stand_alone(q, M):
     """Rows with an infinity or a NaN give NaN in their own row only, rows of zeros the bias; a row does
     not depend on the rows beside it or on the workspace's size."""
     import torch
     rng = np.random.default_rng(M)
-    N, K = 600, 1040
+    N, K = 4200, 1040
     x = _rows(rng, M, K, "float32")
     codes, scales = _weights(rng, N, K)
     wt, st = _t(codes), _t(scales)

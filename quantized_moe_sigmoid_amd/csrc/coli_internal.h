@@ -310,11 +310,11 @@ int64_t i8_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared);  // mo
 struct SortArgs {
   const int32_t *idx;
   int32_t P, E, chunk;
-  int32_t *hist;  // workspace [chunks][E + 1]
+  int32_t *hist;  // workspace [chunks][E + 1]; null: every workgroup counts all pairs
   int32_t *off, *perm, *pos, *active, *nact;
 };
-int sort_chunks(int64_t P);       // workgroups, each with a row of counts in the workspace
-int sort_most_chunks(int64_t P);  // the most of any number of pairs up to P
+constexpr int SORT_CHUNKS = 64;  // most workgroups, each with a row of counts in the workspace
+int sort_chunks(int64_t P);
 hipError_t launch_sort_pairs(SortArgs a, hipStream_t s);
 
 struct PairArgs {
@@ -330,6 +330,7 @@ hipError_t launch_pair_grad(const PairArgs &a, int dtype, const void *dout, cons
 
 struct RouteGradArgs {
   int32_t T, E, k, softmax, renorm;
+  int32_t many;  // set by the launcher: k rounded up to a power of two
   float scale;
   const int32_t *idx;
   const float *dw;

@@ -225,8 +225,8 @@ int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const
 
 size_t coli_moe_sort_pairs_workspace_bytes(int64_t P, int32_t n_experts) {
   if (P < 0 || P >= (1 << 30) || n_experts <= 0 || n_experts > 1024) return 0;
-  // fewer pairs may be cut into more chunks than P of them, up to the most chunks there are
-  return i8_al256((size_t)sort_most_chunks(P) * (n_experts + 1) * sizeof(int32_t));
+  // as many chunks as there are at most: enough for fewer pairs too
+  return i8_al256((size_t)SORT_CHUNKS * (n_experts + 1) * sizeof(int32_t));
 }
 
 int coli_moe_sort_pairs(const int32_t *topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t *expert_off,

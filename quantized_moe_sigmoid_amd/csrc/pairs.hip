@@ -3,29 +3,31 @@
 //
 // All bound by memory: a row is read once for each use and written once. Sums are fp32 in slot order,
 // without atomics.
-#include "group_impl.h"
 #include "mxfp4_impl.h"
 
 namespace coli {
 
 // ------------------------------------------------------------------ sorting
-// A stable counting sort in chunks of pairs: counts of every chunk (sort_count_kernel), then each
-// chunk's workgroup adds up what lies before its own pairs and places them. One chunk needs no counts
-// of others. A wavefront owns consecutive pairs and ranks 64 at a time by ballots (group_impl.h).
-constexpr int SORT_WAVES = 4, SORT_NT = 64 * SORT_WAVES;
+// A stable counting sort in chunks of pairs, a workgroup each: it counts the pairs before its chunk, in
+// it and behind it, which gives every expert's first place, then places its own. A wavefront owns
+// consecutive pairs and ranks 64 at a time by ballots. With many pairs the chunks' counts come from a
+// kernel of their own (sort_count_kernel), else every workgroup counts all pairs.
+constexpr int SORT_WAVES = 16, SORT_NT = 64 * SORT_WAVES;
+
+// One more of expert e of E in cnt; -1 if e is neither an expert nor an empty slot
+__device__ __forceinline__ int sort_count(int *cnt, int e, int E) {
+  if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);
+  else if (e != -1) return -1;
+  return 0;
+}
 
 __global__ __launch_bounds__(SORT_NT) void sort_count_kernel(SortArgs a) {
   extern __shared__ int cnt[];  // [E + 1], the last one: ids out of range
   for (int e = threadIdx.x; e <= a.E; e += SORT_NT) cnt[e] = 0;
   __syncthreads();
   const int first = blockIdx.x * a.chunk, end = min(a.P, first + a.chunk);
-  for (int p = first + threadIdx.x; p < end; p += SORT_NT) {
-    const int e = a.idx[p];
-    if (e >= 0 && e < a.E)
-      atomicAdd(&cnt[e], 1);
-    else if (e != -1)
-      cnt[a.E] = 1;
-  }
+  for (int p = first + threadIdx.x; p < end; p += SORT_NT)
+    if (sort_count(cnt, a.idx[p], a.E) < 0) cnt[a.E] = 1;
   __syncthreads();
   for (int e = threadIdx.x; e <= a.E; e += SORT_NT) a.hist[(int64_t)blockIdx.x * (a.E + 1) + e] = cnt[e];
 }
@@ -41,98 +43,105 @@ __device__ __forceinline__ uint64_t same_id(int id, int bits) {
 }
 
 __global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
-  extern __shared__ int at[];  // [SORT_WAVES][E]: counts, then the next place, of each wavefront's pairs
+  // before [E], total [E]: pairs in earlier chunks, in all; at [SORT_WAVES][E]: counts, then the next
+  // place, of each wavefront's pairs
+  extern __shared__ int before[];
   __shared__ int wsum[SORT_WAVES], wsum2[SORT_WAVES], bad;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, E = a.E;
+  int *total = before + E, *at = total + E, *mine = at + wv * E;
   const int c = blockIdx.x, chunks = gridDim.x;
-  const int seg = a.chunk / SORT_WAVES, first = min(a.P, c * a.chunk + wv * seg), end = min(a.P, first + seg);
+  const int begin = c * a.chunk, behind = min(a.P, begin + a.chunk);
+  const int seg = a.chunk / SORT_WAVES, first = min(a.P, begin + wv * seg), end = min(a.P, first + seg);
   if (tid == 0) bad = 0;
-  for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) at[i] = 0;
+  for (int i = tid; i < (SORT_WAVES + 2) * E; i += SORT_NT) before[i] = 0;
   __syncthreads();
-  for (int p = first + lane; p < end; p += 64) {
-    const int e = a.idx[p];
-    if (e >= 0 && e < E)
-      atomicAdd(&at[wv * E + e], 1);
-    else if (e != -1)
-      bad = 1;
-  }
-  __syncthreads();
-  // experts e0 .. e1 - 1 of this thread
-  const int ept = (E + SORT_NT - 1) / SORT_NT, e0 = min(E, tid * ept), e1 = min(E, e0 + ept);
-  int before[4], total[4], sum = 0, hit = 0;  // E <= 1024
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    before[i] = total[i] = 0;
-    if (e0 + i >= e1) continue;
-    if (chunks == 1) {
-      for (int w = 0; w < SORT_WAVES; w++) total[i] += at[w * E + e0 + i];
-    } else {
-      for (int o = 0; o < chunks; o++) {
-        const int n = a.hist[(int64_t)o * (E + 1) + e0 + i];
-        total[i] += n;
-        before[i] += o < c ? n : 0;
+  int wrong = 0;
+  for (int p = first + lane; p < end; p += 64) wrong |= sort_count(mine, a.idx[p], E);
+  if (a.hist) {
+    // rows of counts: a wavefront takes each sixteenth
+    for (int e0 = 0; e0 <= E; e0 += 64) {
+      const int e = e0 + lane;
+      if (e > E) continue;
+      int sum = 0, less = 0;
+#pragma unroll 4
+      for (int o = wv; o < chunks; o += SORT_WAVES) {
+        const int n = a.hist[(int64_t)o * (E + 1) + e];
+        sum += n;
+        less += o < c ? n : 0;
       }
+      if (e == E) wrong |= -(sum > 0);
+      else if (sum) atomicAdd(&total[e], sum), atomicAdd(&before[e], less);
     }
-    sum += total[i];
-    hit += total[i] > 0;
+  } else {
+    for (int p = tid; p < begin; p += SORT_NT) wrong |= sort_count(before, a.idx[p], E);
+    for (int p = behind + tid; p < a.P; p += SORT_NT) wrong |= sort_count(total, a.idx[p], E);
   }
-  int incl = sum, hincl = hit;
+  if (wrong) bad = 1;
+  __syncthreads();
+  // thread e: expert e (E <= SORT_NT)
+  int n = 0, less = 0;
+  if (tid < E) {
+    less = before[tid];
+    if (a.hist) n = total[tid];
+    else {
+      n = less + total[tid];
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; w++) n += at[w * E + tid];
+    }
+  }
+  const int hit = n > 0;
+  int incl = n, hincl = hit;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int x = __shfl_up(incl, o), y = __shfl_up(hincl, o);
     if (lane >= o) incl += x, hincl += y;
   }
   if (lane == 63) wsum[wv] = incl, wsum2[wv] = hincl;
-  if (chunks > 1 && c == 0)
-    for (int o = tid; o < chunks; o += SORT_NT)
-      if (a.hist[(int64_t)o * (E + 1) + E]) bad = 1;
   __syncthreads();
-  int run = incl - sum, hrun = hincl - hit;
-  for (int i = 0; i < wv; i++) run += wsum[i], hrun += wsum2[i];
+  int run = incl - n, hrun = hincl - hit;
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    if (e0 + i >= e1) continue;
+  for (int i = 0; i < SORT_WAVES; i++)
+    if (i < wv) run += wsum[i], hrun += wsum2[i];
+  if (tid < E) {
     if (c == 0) {
-      a.off[e0 + i] = run;
-      if (total[i] > 0) a.active[hrun++] = e0 + i;
+      a.off[tid] = run;
+      if (hit) a.active[hrun] = tid;
+      if (tid == E - 1) {
+        a.off[E] = run + n;
+        *a.nact = bad ? -1 : hrun + hit;
+      }
     }
-    int place = run + before[i];
+    int place = run + less;
+#pragma unroll
     for (int w = 0; w < SORT_WAVES; w++) {
-      const int n = at[w * E + e0 + i];
-      at[w * E + e0 + i] = place;
-      place += n;
+      const int m = at[w * E + tid];
+      at[w * E + tid] = place;
+      place += m;
     }
-    run += total[i];
-  }
-  if (c == 0 && e0 < e1 && e1 == E) {
-    a.off[E] = run;
-    *a.nact = bad ? -1 : hrun;
   }
   __syncthreads();
   const int bits = 32 - __builtin_clz(E);  // ids 0 .. E, E: none
   for (int p0 = first; p0 < end; p0 += 64) {
     const int p = p0 + lane;
-    int e = p < end ? a.idx[p] : -1;
-    const bool there = e >= 0 && e < E;
+    const int e = p < end ? a.idx[p] : -1;
+    const bool there = (unsigned)e < (unsigned)E;
     const uint64_t who = same_id(there ? e : E, bits);
     const int rank = __popcll(who & ((1ull << lane) - 1));
     int place = -1;
     if (there) {
-      place = at[wv * E + e] + rank;
+      place = mine[e] + rank;
       a.perm[place] = p;
     }
     if (p < end) a.pos[p] = place;
     __builtin_amdgcn_wave_barrier();
-    if (there && rank == 0) at[wv * E + e] = place + __popcll(who);
+    if (there && rank == 0) mine[e] = place + __popcll(who);
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-// Pairs of a chunk: a multiple of 64 for each wavefront, and so many that no more than SORT_CHUNKS
-// rows of counts are read by every workgroup
-constexpr int SORT_CHUNKS = 128, SORT_ONE = 1024;
+// Pairs of a chunk: 64 for each wavefront, or so many that there are no more than SORT_CHUNKS chunks
+constexpr int SORT_SELF = 32768;
 static int sort_chunk(int64_t P) {
-  if (P <= SORT_ONE) return SORT_ONE;
   const int64_t c = (P + SORT_CHUNKS - 1) / SORT_CHUNKS;
   return (int)((c + SORT_NT - 1) / SORT_NT * SORT_NT);
 }
@@ -140,103 +149,157 @@ int sort_chunks(int64_t P) {
   const int c = sort_chunk(P);
   return (int)((P + c - 1) / c);
 }
-int sort_most_chunks(int64_t P) {
-  if (P <= SORT_ONE) return 1;
-  return P < (int64_t)SORT_CHUNKS * SORT_NT ? (int)((P + SORT_NT - 1) / SORT_NT) : SORT_CHUNKS;
-}
 
 hipError_t launch_sort_pairs(SortArgs a, hipStream_t s) {
   a.chunk = sort_chunk(a.P);
   const int chunks = sort_chunks(a.P);
-  if (chunks > 1) {
+  if (a.P <= SORT_SELF) {
+    a.hist = nullptr;
+  } else {
     hipLaunchKernelGGL(sort_count_kernel, dim3(chunks), dim3(SORT_NT), (a.E + 1) * sizeof(int), s, a);
     if (const hipError_t st = hipGetLastError(); st != hipSuccess) return st;
   }
-  hipLaunchKernelGGL(sort_place_kernel, dim3(chunks), dim3(SORT_NT), (size_t)SORT_WAVES * a.E * sizeof(int), s, a);
+  const size_t lds = (size_t)(SORT_WAVES + 2) * a.E * sizeof(int);  // 72 KB for 1024 experts
+  static PerDevice allowed;
+  if (const hipError_t st = allow_lds(allowed, sort_place_kernel, (SORT_WAVES + 2) * 1024 * sizeof(int)); st != hipSuccess) return st;
+  hipLaunchKernelGGL(sort_place_kernel, dim3(chunks), dim3(SORT_NT), lds, s, a);
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ rows
 // A thread takes one piece (16 bytes, or one element where rows are not whole aligned pieces) of a
-// token's row for all of its slots.
-template <typename U>
-__global__ __launch_bounds__(256) void dispatch_kernel(const U *__restrict__ x, uint32_t T_, int k, uint32_t units,
-                                                       const int32_t *__restrict__ pos, int64_t rows,
-                                                       U *__restrict__ xs) {
-  const int64_t n = (int64_t)T_ * units, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-    const int64_t t = i / units;
-    const uint32_t u = (uint32_t)(i - t * units);
-    const U v = x[i];
-    for (int j = 0; j < k; j++) {
-      const int64_t r = pos[t * k + j];
-      if (r >= 0 && r < rows) xs[r * units + u] = v;
-    }
+// pair's row, or of a token's. Rows of pairs are used once and pass the caches by.
+template <typename T, int VEC>
+struct VecOf {
+  typedef T type __attribute__((ext_vector_type(VEC)));
+};
+template <typename T>
+struct VecOf<T, 1> {
+  typedef T type;
+};
+template <typename T, int VEC>
+using piece_of = typename VecOf<T, VEC>::type;
+
+template <typename T, int VEC>
+__device__ __forceinline__ T part(const piece_of<T, VEC> &x, int e) {
+  if constexpr (VEC == 1) return x;
+  else return x[e];
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void set_part(piece_of<T, VEC> &x, int e, T y) {
+  if constexpr (VEC == 1) x = y;
+  else x[e] = y;
+}
+
+// i = row * units + u; WIDE: i may pass 32 bits
+template <bool WIDE>
+__device__ __forceinline__ void split(int64_t i, uint32_t units, int64_t &row, uint32_t &u) {
+  if constexpr (WIDE) {
+    row = i / units;
+    u = (uint32_t)(i - row * units);
+  } else {
+    const uint32_t r = (uint32_t)i / units;
+    row = r;
+    u = (uint32_t)i - r * units;
   }
 }
 
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Piece {
-  T v[VEC];
-};
+template <typename U, bool WIDE>
+__global__ __launch_bounds__(256) void dispatch_kernel(const U *__restrict__ x, int64_t P, uint32_t k, uint32_t units,
+                                                       const int32_t *__restrict__ pos, int64_t rows,
+                                                       U *__restrict__ xs) {
+  const int64_t n = P * units, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    int64_t p;
+    uint32_t u;
+    split<WIDE>(i, units, p, u);
+    const int64_t r = pos[p];
+    if (r >= 0 && r < rows) __builtin_nontemporal_store(x[(int64_t)((uint32_t)p / k) * units + u], xs + r * units + u);
+  }
+}
 
-template <typename T, int VEC>
-__global__ __launch_bounds__(256) void combine_kernel_t(const Piece<T, VEC> *__restrict__ ys, int64_t rows, uint32_t T_,
-                                                        int k, uint32_t units, const int32_t *__restrict__ pos,
-                                                        const float *__restrict__ w,
-                                                        const Piece<T, VEC> *__restrict__ add,
-                                                        Piece<T, VEC> *__restrict__ out) {
+constexpr int SLOTS = 8;  // rows of a token under way at a time
+
+template <typename T, int VEC, bool WIDE>
+__global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC> *__restrict__ ys, int64_t rows, uint32_t T_,
+                                                           int k, uint32_t units, const int32_t *__restrict__ pos,
+                                                           const float *__restrict__ w,
+                                                           const piece_of<T, VEC> *__restrict__ add,
+                                                           piece_of<T, VEC> *__restrict__ out) {
+  typedef piece_of<T, VEC> piece;
   const int64_t n = (int64_t)T_ * units, step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-    const int64_t t = i / units;
-    const uint32_t u = (uint32_t)(i - t * units);
+    int64_t t;
+    uint32_t u;
+    split<WIDE>(i, units, t, u);
     float s[VEC] = {};
-    for (int j = 0; j < k; j++) {
-      const int64_t r = pos[t * k + j];
-      if (r < 0 || r >= rows) continue;
-      const Piece<T, VEC> y = ys[r * units + u];
-      const float wt = w ? w[t * k + j] : 1.0f;
+    for (int j0 = 0; rows > 0 && j0 < k; j0 += SLOTS) {
+      piece y[SLOTS];
+      bool there[SLOTS];
 #pragma unroll
-      for (int e = 0; e < VEC; e++) s[e] = __builtin_fmaf(wt, (float)y.v[e], s[e]);
+      for (int j = 0; j < SLOTS; j++) {  // an empty slot reads row 0 and leaves the sum as it is
+        const int64_t r = j0 + j < k ? pos[t * k + j0 + j] : -1;
+        there[j] = r >= 0 && r < rows;
+        y[j] = __builtin_nontemporal_load(ys + (there[j] ? r : 0) * units + u);
+      }
+#pragma unroll
+      for (int j = 0; j < SLOTS; j++) {
+        if (!there[j]) continue;
+        const float wt = w ? w[t * k + j0 + j] : 1.0f;
+#pragma unroll
+        for (int e = 0; e < VEC; e++) s[e] = __builtin_fmaf(wt, (float)part<T, VEC>(y[j], e), s[e]);
+      }
     }
     if (add) {
-      const Piece<T, VEC> y = add[i];
+      const piece y = add[i];
 #pragma unroll
-      for (int e = 0; e < VEC; e++) s[e] += (float)y.v[e];
+      for (int e = 0; e < VEC; e++) s[e] += (float)part<T, VEC>(y, e);
     }
-    Piece<T, VEC> o;
+    piece o;
 #pragma unroll
-    for (int e = 0; e < VEC; e++) o.v[e] = (T)s[e];
+    for (int e = 0; e < VEC; e++) set_part<T, VEC>(o, e, (T)s[e]);
     out[i] = o;
   }
 }
 
 // A wavefront takes a pair: its row of the gradient, and the weight's
+constexpr int GRAD_AHEAD = 4;  // pieces of a lane under way
 template <typename T, int VEC>
-__global__ __launch_bounds__(256) void combine_grad_kernel(const Piece<T, VEC> *__restrict__ dout,
-                                                           const Piece<T, VEC> *__restrict__ ys, int64_t rows, uint32_t P,
+__global__ __launch_bounds__(256) void combine_grad_kernel(const piece_of<T, VEC> *__restrict__ dout,
+                                                           const piece_of<T, VEC> *__restrict__ ys, int64_t rows, uint32_t P,
                                                            int k, uint32_t units, const int32_t *__restrict__ pos,
-                                                           const float *__restrict__ w, Piece<T, VEC> *__restrict__ dys,
+                                                           const float *__restrict__ w, piece_of<T, VEC> *__restrict__ dys,
                                                            float *__restrict__ dw) {
+  typedef piece_of<T, VEC> piece;
   const int lane = threadIdx.x & 63;
   for (uint32_t p = blockIdx.x * 4 + (threadIdx.x >> 6); p < P; p += gridDim.x * 4) {
     const int64_t r = pos[p];
     float sum = 0.0f;
     if (r >= 0 && r < rows) {
       const float wt = w[p];
-      const Piece<T, VEC> *d = dout + (int64_t)(p / k) * units;
-      for (uint32_t u = lane; u < units; u += 64) {
-        const Piece<T, VEC> g = d[u];
-        if (dw) {
-          const Piece<T, VEC> y = ys[r * units + u];
+      const piece *d = dout + (int64_t)(p / k) * units, *yr = ys + r * units;
+      for (uint32_t u0 = lane; u0 < units; u0 += 64 * GRAD_AHEAD) {
+        piece g[GRAD_AHEAD], y[GRAD_AHEAD];
 #pragma unroll
-          for (int e = 0; e < VEC; e++) sum = __builtin_fmaf((float)g.v[e], (float)y.v[e], sum);
+        for (int a = 0; a < GRAD_AHEAD; a++) {
+          const uint32_t u = min(u0 + 64 * a, units - 1);
+          g[a] = d[u];
+          if (dw) y[a] = __builtin_nontemporal_load(yr + u);
         }
-        if (dys) {
-          Piece<T, VEC> o;
 #pragma unroll
-          for (int e = 0; e < VEC; e++) o.v[e] = (T)(wt * (float)g.v[e]);
-          dys[r * units + u] = o;
+        for (int a = 0; a < GRAD_AHEAD; a++) {
+          const uint32_t u = u0 + 64 * a;
+          if (u >= units) break;
+          if (dw) {
+#pragma unroll
+            for (int e = 0; e < VEC; e++) sum = __builtin_fmaf((float)part<T, VEC>(g[a], e), (float)part<T, VEC>(y[a], e), sum);
+          }
+          if (dys) {
+            piece o;
+#pragma unroll
+            for (int e = 0; e < VEC; e++) set_part<T, VEC>(o, e, (T)(wt * (float)part<T, VEC>(g[a], e)));
+            __builtin_nontemporal_store(o, dys + r * units + u);
+          }
         }
       }
     }
@@ -259,23 +322,25 @@ hipError_t launch_dispatch(const PairArgs &a, int dtype, const void *x, void *xs
   const int size = dtype == COLI_F32 ? 4 : 2;
   auto go = [&]<typename U>() {
     const uint32_t units = (uint32_t)((int64_t)a.H * size / (int)sizeof(U));
-    const int64_t n = (int64_t)a.T * units;
-    hipLaunchKernelGGL(dispatch_kernel<U>, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const U *)x, (uint32_t)a.T,
-                       a.k, units, a.pos, a.rows, (U *)xs);
+    const int64_t P = (int64_t)a.T * a.k, n = P * units;
+    auto kernel = n < ((int64_t)1 << 32) ? dispatch_kernel<U, false> : dispatch_kernel<U, true>;
+    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const U *)x, P, (uint32_t)a.k, units, a.pos,
+                       a.rows, (U *)xs);
     return hipGetLastError();
   };
-  if (whole(a.H, size, x, xs)) return go.template operator()<uint4>();
+  if (whole(a.H, size, x, xs)) return go.template operator()<v4i32>();
   return size == 4 ? go.template operator()<uint32_t>() : go.template operator()<uint16_t>();
 }
 
 template <typename T>
 static hipError_t launch_combine_t(const PairArgs &a, const void *ys, const void *add, void *out, hipStream_t s) {
   auto go = [&]<int VEC>() {
-    typedef Piece<T, VEC> piece;
+    typedef piece_of<T, VEC> piece;
     const uint32_t units = (uint32_t)(a.H / VEC);
     const int64_t n = (int64_t)a.T * units;
-    hipLaunchKernelGGL((combine_kernel_t<T, VEC>), dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const piece *)ys,
-                       a.rows, (uint32_t)a.T, a.k, units, a.pos, a.w, (const piece *)add, (piece *)out);
+    auto kernel = n < ((int64_t)1 << 32) ? pair_combine_kernel<T, VEC, false> : pair_combine_kernel<T, VEC, true>;
+    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const piece *)ys, a.rows, (uint32_t)a.T, a.k,
+                       units, a.pos, a.w, (const piece *)add, (piece *)out);
     return hipGetLastError();
   };
   return whole(a.H, sizeof(T), ys, out, add) ? go.template operator()<16 / sizeof(T)>() : go.template operator()<1>();
@@ -290,7 +355,7 @@ hipError_t launch_pair_combine(const PairArgs &a, int dtype, const void *ys, con
 template <typename T>
 static hipError_t launch_grad_t(const PairArgs &a, const void *dout, const void *ys, void *dys, float *dw, hipStream_t s) {
   auto go = [&]<int VEC>() {
-    typedef Piece<T, VEC> piece;
+    typedef piece_of<T, VEC> piece;
     const uint32_t units = (uint32_t)(a.H / VEC), P = (uint32_t)a.T * (uint32_t)a.k;
     hipLaunchKernelGGL((combine_grad_kernel<T, VEC>), dim3(groups_of((P + 3) / 4)), dim3(256), 0, s, (const piece *)dout,
                        (const piece *)ys, a.rows, P, a.k, units, a.pos, a.w, (piece *)dys, dw);

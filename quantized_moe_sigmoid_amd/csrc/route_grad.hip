@@ -17,16 +17,16 @@ namespace coli {
 
 constexpr int RG_WAVES = 4;
 
-__device__ __forceinline__ double wave_total(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
 __device__ __forceinline__ double lane_value(double v, int lane) {
   const uint64_t u = __double_as_longlong(v);
   const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
   return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// Sum of the values of the first `many` lanes (a power of two), the others holding 0; in every lane
+__device__ __forceinline__ double lanes_total(double v, int many) {
+  for (int o = many >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return lane_value(v, 0);
 }
 
 // z and dz may be one array: a wavefront has read its row before it writes it
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(64 * RG_WAVES) void route_grad_kernel(RouteGradArgs
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * RG_WAVES + (threadIdx.x >> 6);
   if (t >= a.T) return;
-  const int E = a.E, k = a.k;
+  const int E = a.E, k = a.k, many = a.many;
   const T *zt = z + t * E;
   float v[EPL];  // -inf: not there
   float top = -INFINITY;
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * RG_WAVES) void route_grad_kernel(RouteGradArgs
         p[i] = some && v[i] > -INFINITY ? exp((double)v[i] - (double)top) : 0.0;
         total += p[i];
       }
-      total = wave_total(total);
+      total = lanes_total(total, 64);
       const double inv = total > 0.0 ? 1.0 / total : 0.0;
 #pragma unroll
       for (int i = 0; i < EPL; i++) p[i] *= inv;
@@ -79,12 +79,12 @@ __global__ __launch_bounds__(64 * RG_WAVES) void route_grad_kernel(RouteGradArgs
   // what this lane's slot gives its expert
   double mean = 0.0, give;
   if (a.renorm) {
-    const double total = wave_total(ps);
+    const double total = lanes_total(ps, many);
     const double share = total > 0.0 ? ps / total : 0.0;
-    mean = wave_total(share > 0.0 ? g * share : 0.0);
+    mean = lanes_total(share > 0.0 ? g * share : 0.0, many);
     give = share > 0.0 ? (double)a.scale * (g - mean) * share * rest : 0.0;
   } else if constexpr (SOFTMAX) {
-    mean = wave_total(ps > 0.0 ? g * ps : 0.0) * (double)a.scale;
+    mean = lanes_total(ps > 0.0 ? g * ps : 0.0, many) * (double)a.scale;
     give = g * (double)a.scale;
   } else {
     give = ps > 0.0 ? (double)a.scale * g * ps * rest : 0.0;
@@ -106,7 +106,8 @@ __global__ __launch_bounds__(64 * RG_WAVES) void route_grad_kernel(RouteGradArgs
 }
 
 template <typename T>
-static hipError_t launch_rg(const RouteGradArgs &a, const T *z, T *dz, hipStream_t s) {
+static hipError_t launch_rg(RouteGradArgs a, const T *z, T *dz, hipStream_t s) {
+  for (a.many = 1; a.many < a.k;) a.many *= 2;
   const dim3 grid((unsigned)((a.T + RG_WAVES - 1) / RG_WAVES)), block(64 * RG_WAVES);
   auto go = [&]<int EPL>() {
     if (a.softmax)

@@ -168,7 +168,7 @@ hipError_t launch_sort_pairs(SortArgs a, hipStream_t s) {
 
 // ------------------------------------------------------------------ rows
 // A thread takes one piece (16 bytes, or one element where rows are not whole aligned pieces) of a
-// pair's row, or of a token's. Rows of pairs are used once and pass the caches by.
+// token's row, for all of its slots. Rows of pairs are used once and pass the caches by.
 template <typename T, int VEC>
 struct VecOf {
   typedef T type __attribute__((ext_vector_type(VEC)));
@@ -204,21 +204,28 @@ __device__ __forceinline__ void split(int64_t i, uint32_t units, int64_t &row, u
   }
 }
 
+constexpr int SLOTS = 8;  // rows of a token under way at a time
+
 template <typename U, bool WIDE>
-__global__ __launch_bounds__(256) void dispatch_kernel(const U *__restrict__ x, int64_t P, uint32_t k, uint32_t units,
+__global__ __launch_bounds__(256) void dispatch_kernel(const U *__restrict__ x, uint32_t T_, int k, uint32_t units,
                                                        const int32_t *__restrict__ pos, int64_t rows,
                                                        U *__restrict__ xs) {
-  const int64_t n = P * units, step = (int64_t)gridDim.x * 256;
+  const int64_t n = (int64_t)T_ * units, step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-    int64_t p;
+    int64_t t;
     uint32_t u;
-    split<WIDE>(i, units, p, u);
-    const int64_t r = pos[p];
-    if (r >= 0 && r < rows) __builtin_nontemporal_store(x[(int64_t)((uint32_t)p / k) * units + u], xs + r * units + u);
+    split<WIDE>(i, units, t, u);
+    const U v = x[i];
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
+      int64_t r[SLOTS];
+#pragma unroll
+      for (int j = 0; j < SLOTS; j++) r[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+#pragma unroll
+      for (int j = 0; j < SLOTS; j++)
+        if (r[j] >= 0 && r[j] < rows) __builtin_nontemporal_store(v, xs + r[j] * units + u);
+    }
   }
 }
-
-constexpr int SLOTS = 8;  // rows of a token under way at a time
 
 template <typename T, int VEC, bool WIDE>
 __global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC> *__restrict__ ys, int64_t rows, uint32_t T_,
@@ -233,14 +240,14 @@ __global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC
     uint32_t u;
     split<WIDE>(i, units, t, u);
     float s[VEC] = {};
-    for (int j0 = 0; rows > 0 && j0 < k; j0 += SLOTS) {
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
       piece y[SLOTS];
       bool there[SLOTS];
 #pragma unroll
-      for (int j = 0; j < SLOTS; j++) {  // an empty slot reads row 0 and leaves the sum as it is
+      for (int j = 0; j < SLOTS; j++) {
         const int64_t r = j0 + j < k ? pos[t * k + j0 + j] : -1;
         there[j] = r >= 0 && r < rows;
-        y[j] = __builtin_nontemporal_load(ys + (there[j] ? r : 0) * units + u);
+        if (there[j]) y[j] = __builtin_nontemporal_load(ys + r * units + u);
       }
 #pragma unroll
       for (int j = 0; j < SLOTS; j++) {
@@ -258,12 +265,12 @@ __global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC
     piece o;
 #pragma unroll
     for (int e = 0; e < VEC; e++) set_part<T, VEC>(o, e, (T)s[e]);
-    out[i] = o;
+    __builtin_nontemporal_store(o, out + i);
   }
 }
 
 // A wavefront takes a pair: its row of the gradient, and the weight's
-constexpr int GRAD_AHEAD = 4;  // pieces of a lane under way
+constexpr int GRAD_AHEAD = 8;  // pieces of a lane under way
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const piece_of<T, VEC> *__restrict__ dout,
                                                            const piece_of<T, VEC> *__restrict__ ys, int64_t rows, uint32_t P,
@@ -322,9 +329,9 @@ hipError_t launch_dispatch(const PairArgs &a, int dtype, const void *x, void *xs
   const int size = dtype == COLI_F32 ? 4 : 2;
   auto go = [&]<typename U>() {
     const uint32_t units = (uint32_t)((int64_t)a.H * size / (int)sizeof(U));
-    const int64_t P = (int64_t)a.T * a.k, n = P * units;
+    const int64_t n = (int64_t)a.T * units;
     auto kernel = n < ((int64_t)1 << 32) ? dispatch_kernel<U, false> : dispatch_kernel<U, true>;
-    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const U *)x, P, (uint32_t)a.k, units, a.pos,
+    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const U *)x, (uint32_t)a.T, a.k, units, a.pos,
                        a.rows, (U *)xs);
     return hipGetLastError();
   };

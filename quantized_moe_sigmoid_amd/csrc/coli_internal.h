@@ -303,6 +303,9 @@ hipError_t launch_i8_quantize(const void *x, int dtype, int64_t rows, int K, int
                               hipStream_t s);
 hipError_t launch_i8_gemv(I8Mode mode, int dtype, const I8Args &a, hipStream_t s);
 bool i8_gemv_from_x(const I8Args &a);  // launch_i8_gemv with x set takes these sizes
+bool i8_down_fused(const I8Args &a);   // launch_i8_down takes these sizes, with x set:
+bool i8_down_from_x(const I8Args &a);
+hipError_t launch_i8_down(const I8Args &a, const int32_t *idx, const float *w, void *out, int dtype, hipStream_t s);
 hipError_t launch_i8_tile(I8Mode mode, int dtype, const I8Args &a, hipStream_t s);
 int64_t i8_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared);  // most row tiles of a route
 

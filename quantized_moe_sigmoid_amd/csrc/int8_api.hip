@@ -214,9 +214,14 @@ int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const
   a.K = cfg->ffn;
   int8_t *aq = reinterpret_cast<int8_t *>(ws + L.aq);
   float *as = reinterpret_cast<float *>(ws + L.as), *y = reinterpret_cast<float *>(ws + L.y);
-  if ((st = i8_dev(launch_i8_quantize(h, dtype, i8_rows(*cfg, T), cfg->ffn, i8_padded(cfg->ffn), aq, as, s)))) return st;
+  const bool fused = i8_down_fused(a);
+  if (fused && i8_down_from_x(a))
+    a.x = h;
+  else if ((st = i8_dev(launch_i8_quantize(h, dtype, i8_rows(*cfg, T), cfg->ffn, i8_padded(cfg->ffn), aq, as, s))))
+    return st;
   a.aq = aq;
   a.as = as;
+  if (fused) return i8_dev(launch_i8_down(a, topk_idx, topk_w, out, dtype, s));
   a.out = y;
   if ((st = i8_dev(launch_experts(I8_DOWN, dtype, a, ws, L, s)))) return st;
   return i8_dev(launch_mx_combine(y, topk_idx, topk_w, T, cfg->top_k, cfg->n_experts, cfg->hidden, cfg->has_shared, out,

@@ -14,24 +14,42 @@ __device__ __forceinline__ float i8_scale(uint32_t top) {
   return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 127.0f;
 }
 
-// Code of v; inv is about 1 / s (within 2^-22). |v / s| <= 127, so v inv is within 2^-15 of the
-// quotient: away from a half its nearest integer is the quotient's, near one the division decides.
-// Scales of 0, below 2^-126 or NaN: inv is infinite or NaN, and so is what follows.
-__device__ __forceinline__ int i8_code(float v, float s, float inv) {
-  const float r = v * inv;
-  float q = __builtin_rintf(r);
-  if (__builtin_expect(!(fabsf(r - q) <= 0.4999f), 0)) {
-    q = roundf(v / s);
-    q = s > 0.0f ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
-  }
-  return (int)q;
+// What a row is rounded with: its scale s and about 1 / s (within 2^-23 of it), NaN where s is 0, below
+// fp32's normal numbers or NaN.
+struct I8Row {
+  float s, inv;
+};
+__device__ __forceinline__ I8Row i8_row(uint32_t top) {
+  const float s = i8_scale(top);
+  return I8Row{s, s >= 0x1p-126f ? __builtin_amdgcn_rcpf(s) : __uint_as_float(0x7FC00000u)};
 }
 
-__device__ __forceinline__ uint2 i8_codes8(const float (&v)[8], float s, float inv) {
-  uint32_t w[2] = {0, 0};
+// The definition: one division, rounded half away from zero
+__device__ __forceinline__ uint32_t i8_code(float v, float s) {
+  return s > 0.0f ? (uint32_t)(int)fminf(fmaxf(roundf(v / s), -127.0f), 127.0f) : 0u;
+}
+
+// Codes of eight values. |v / s| <= 127.001 and v inv is within 2^-15 of the quotient: where it is not
+// that near a half, its nearest integer is the code, and the sum with 3 * 2^22 holds it in its low byte.
+// Otherwise (one value in 5000) and for scales without an inverse the division decides, for all eight.
+__device__ __forceinline__ uint2 i8_codes8(const float (&v)[8], const I8Row &row) {
+  constexpr float M = 0x1.8p+23f;
+  uint32_t w[8];
+  float far = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) w[i >> 2] |= (uint32_t)(i8_code(v[i], s, inv) & 0xFF) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+  for (int i = 0; i < 8; i++) {
+    const float t = __builtin_fmaf(v[i], row.inv, M);
+    far = fmaxf(far, fabsf(__builtin_fmaf(v[i], row.inv, M - t)));
+    w[i] = __float_as_uint(t);
+  }
+  if (__builtin_expect(!(far <= 0.4999f && row.inv == row.inv), 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) w[i] = i8_code(v[i], row.s);
+  }
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) h[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x0c0c0400u);
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 
 __device__ __forceinline__ uint32_t i8_top8(const float (&v)[8], uint32_t top) {

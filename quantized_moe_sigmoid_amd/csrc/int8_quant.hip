@@ -41,18 +41,18 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const T *__restrict__ 
       __syncthreads();
       top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
     }
-    const float s = i8_scale(top), inv = __builtin_amdgcn_rcpf(s);
-    if (l == 0) scales[row] = s;
+    const I8Row r = i8_row(top);
+    if (l == 0) scales[row] = r.s;
     if constexpr (REGS > 0) {
 #pragma unroll
       for (int i = 0; i < REGS; i++) {
         const int u = l + L * i;
-        if (u < n) *reinterpret_cast<uint2 *>(pc + u * 8) = i8_codes8(v[i], s, inv);
+        if (u < n) *reinterpret_cast<uint2 *>(pc + u * 8) = i8_codes8(v[i], r);
       }
     } else {
       for (int u = l; u < n; u += L) {
         load8(px + u * 8, v[0]);
-        *reinterpret_cast<uint2 *>(pc + u * 8) = i8_codes8(v[0], s, inv);
+        *reinterpret_cast<uint2 *>(pc + u * 8) = i8_codes8(v[0], r);
       }
     }
     for (int u = n + l; u < np; u += L) *reinterpret_cast<uint2 *>(pc + u * 8) = make_uint2(0, 0);

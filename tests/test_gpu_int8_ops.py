@@ -233,7 +233,9 @@ EXPERTS = [  # T, H, F, E, k, shared, dropped
     (1, 256, 128, 4, 2, False, False), (1, 1280, 384, 16, 8, True, False), (3, 640, 256, 8, 3, True, True),
     (17, 384, 640, 16, 4, True, False), (40, 512, 256, 5, 1, False, True), (70, 256, 384, 64, 8, True, True),
     (130, 896, 128, 3, 2, True, False), (300, 384, 512, 16, 4, True, True), (600, 256, 256, 60, 6, False, False),
-    (90, 512, 384, 200, 7, True, True), (257, 640, 896, 2, 2, False, True)]
+    (90, 512, 384, 200, 7, True, True), (257, 640, 896, 2, 2, False, True),
+    (1, 6144, 2048, 12, 8, True, False), (2, 2048, 1024, 64, 8, False, True), (16, 1024, 1408, 100, 16, True, True), (15, 896, 256, 1024, 17, True, False),
+    (33, 640, 2048, 256, 8, False, False), (64, 384, 128, 500, 12, True, True), (49, 6144, 256, 64, 2, True, False)]
 
 
 def _case(rng, T, H, F, E, k, shared, dropped, unused=True):
@@ -328,6 +330,34 @@ def test_down(q, dtype, T, H, F, E, k, shared, dropped):
     # 3 roundings of a pair's row, a product and an addition for each slot, the output's rounding
     tol = (3 + 1 + k + 1) * U * size
     assert (np.abs(got - want) <= tol + _half(dtype) * (np.abs(want) + tol) + _tiny(dtype)).all()
+
+
+@pytest.mark.parametrize("T,k", [(1, 4), (5, 3), (16, 6), (40, 5)])
+def test_down_expert_twice_in_a_token(q, T, k):
+    """Slots of one token that hold the same expert, and ids out of range, which are empty slots."""
+    import torch
+    rng = np.random.default_rng(T)
+    H, F, E = 384, 512, 64
+    _, w, codes, scales = _case(rng, T, H, F, E, k, True, False)
+    idx = rng.integers(0, 3 if T < 20 else E, (T, k)).astype(np.int32)
+    idx[T // 2, 0] = -1
+    idx[0, :2] = idx[0, 1]
+    if T > 4:
+        idx[4, 2], idx[3, 1] = E, -5
+    cfg = q.make_cfg(H, F, E, k, has_shared=True, wbits=8)
+    h = _rows(rng, T * (k + 1), F, "float32")
+    out, ws = torch.full((T, H), 9.0, device="cuda"), q.alloc_int8_experts_workspace(cfg, T)
+    g = _grouped(q, np.where((idx >= 0) & (idx < E), idx, -1), E)
+    q.int8_down(cfg, q.Weights(_t(codes), _t(scales), None, None), h, _t(idx), _t(w), **g, out=out, workspace=ws)
+    rc, rs = i8ref.quantise(h.cpu().numpy())
+    want, size = np.zeros((T, H)), np.zeros((T, H))
+    for e, rows, tokens in _rows_of(idx, E, True):
+        y = i8ref.dot(rc[rows], codes[e, 2 * F * H:].reshape(H, F)) * rs[rows].astype(np.float64)[:, None] * scales[e, 2 * F:].astype(np.float64)
+        if e < E:
+            y = y * w.reshape(-1)[rows, None].astype(np.float64)
+        np.add.at(want, tokens, y)
+        np.add.at(size, tokens, np.abs(y))
+    assert (np.abs(_n(out) - want) <= (3 + 1 + k + 1) * U * size + U * np.abs(want)).all()
 
 
 def test_experts_one_token_as_in_a_batch(q):

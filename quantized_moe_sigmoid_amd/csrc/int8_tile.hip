@@ -10,9 +10,12 @@
 
 namespace coli {
 
-// BM x BN tile, WM x WN wavefronts, NBUF K stages of 8 chunks (128 inputs) in LDS, OCC workgroups per CU
-template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int OCC_>
+// BM x BN tile, WM x WN wavefronts, NBUF K stages of 8 chunks (128 inputs) in LDS, OCC workgroups per CU.
+// STRIPS: a workgroup takes column tiles one after another, the next one's loads under way while a tile is
+// written out; else the stages' LDS serves for writing it out.
+template <int BM_, int BN_, int WM_, int WN_, int NBUF_, int OCC_, bool STRIPS_>
 struct I8Shape {
+  static constexpr bool STRIPS = STRIPS_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NBUF = NBUF_, OCC = OCC_;
   static constexpr int KB = 8, KS = 4;                        // chunks of a stage, its K steps of 32 inputs
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;  // 32 x 32 tiles of a wavefront
@@ -20,12 +23,15 @@ struct I8Shape {
   static constexpr int STAGE = (BM + BN) * KB * 16;           // LDS bytes
   static constexpr int IDS = NBUF * STAGE;                    // offset of the row ids
   static constexpr int SCALES = IDS + BM * 4;                 // offset of two sets of channel scales and biases
-  static constexpr int BYTES = SCALES + 2 * 2 * BN * 4;
-  static_assert(LB % 2 == 0);
+  // 32 rows of 128 bytes and a pad for each wavefront, through which results go to whole lines
+  static constexpr int OUT_ROW = 144, OUT_WAVE = 32 * OUT_ROW;
+  static constexpr int OUT = STRIPS ? SCALES + 2 * 2 * BN * 4 : 0;
+  static constexpr int BYTES = SCALES + 2 * 2 * BN * 4 + (STRIPS ? 4 * OUT_WAVE : 0);
+  static_assert(LB % 2 == 0 && 4 * OUT_WAVE <= IDS);
 };
-typedef I8Shape<256, 256, 2, 2, 2, 1> I8Dense;
-typedef I8Shape<128, 128, 1, 4, 2, 2> I8DenseSmall;
-typedef I8Shape<128, 256, 1, 4, 3, 1> I8Experts;
+typedef I8Shape<256, 256, 2, 2, 2, 1, true> I8Dense;
+typedef I8Shape<128, 128, 1, 4, 2, 2, false> I8DenseSmall;
+typedef I8Shape<128, 256, 1, 4, 3, 1, false> I8Experts;
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 
@@ -47,7 +53,7 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
   // the rows of activations: first .. first + n - 1 of perm, or of the tokens; and the column
   // tiles bx .. bx + cols - 1, one after another
   int bx, by, cols, e = 0, first = 0, n = 0;
-  bool routed = false;
+  bool routed = false, once = false;
   if constexpr (MODE == I8_LINEAR) {
     int sx;
     tile_of(blockIdx.x, ns, (a.M + BM - 1) / BM, sx, by);
@@ -72,6 +78,7 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
     first = c.y;
     n = c.z;
     routed = (c.w & 1) != 0;
+    once = grp == 1;
   }
   const int64_t P = (int64_t)a.M * a.k;
   // tile row i -> row of the output, of the activations
@@ -115,7 +122,8 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
   const int li = lane & 31, hh = lane >> 5;
 
-  auto run = [&]<int MX>() {  // with MX 32-row tiles to a wavefront
+  // with MX 32-row tiles to a wavefront; ONCE: no other workgroup reads these weights
+  auto run = [&]<int MX, bool ONCE>() {
     float row_scale[MX];
 #pragma unroll
     for (int i = 0; i < MX; i++) row_scale[i] = as[act_row(wm * (BM / S::WM) + i * 32 + li)];
@@ -151,7 +159,10 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
           dma16(aq + ahead * (KB * 16) - 4096, oa[2 * q], dst, on, on);
       } else {
         const int i = q - QA;
-        dma16_pair(pb + ahead * (KB * 16), ob[2 * i] - past, ob[2 * i + 1] - past, buf + BM * (KB * 16) + (8 * i + wv) * 1024, on, on);
+        if constexpr (ONCE)
+          dma16_pair_once(pb + ahead * (KB * 16), ob[2 * i] - past, ob[2 * i + 1] - past, buf + BM * (KB * 16) + (8 * i + wv) * 1024, on, on);
+        else
+          dma16_pair(pb + ahead * (KB * 16), ob[2 * i] - past, ob[2 * i + 1] - past, buf + BM * (KB * 16) + (8 * i + wv) * 1024, on, on);
       }
     };
     constexpr int ISSUES = QA + QB, LOADS = NA + S::LB;
@@ -249,72 +260,80 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
         __builtin_amdgcn_sched_barrier(0);
       }
       // Results: lane column li (a row of activations) of a 32 x 32 tile, rows (weight rows)
-      // 8 (r / 4) + 4 hh + r % 4, so that a lane holds runs of four output columns. Two bytes to a
-      // value: the halves of the wavefront trade runs and each lane stores eight columns.
+      // 8 (r / 4) + 4 hh + r % 4, so that a lane holds runs of four output columns of a row. They go
+      // through LDS, up to 128 bytes of 32 rows at a time, so that a store covers whole lines: written
+      // from there, a run each, 32 rows' stores would be 32 bytes apart (gate/up of 2048 tokens 1303 us,
+      // 1159 without stores; down 870 and 752; 4093 x 12288 x 6144 298 and 272).
       // The stores have no branch (it would bring all results out of the accumulators at once,
       // as it does for a ragged N, whose last piece's columns go one by one): lanes without a row,
       // and pieces past the last column, give an offset past the buffer's end, where a store is
       // dropped.
       constexpr int GROUPS = MODE == I8_GATEUP ? 2 : 4, WF = BF / S::WN, JF = MODE == I8_GATEUP ? 16 : 32;
+      constexpr int BC = WF * (int)sizeof(T) < 128 ? WF : 128 / (int)sizeof(T);  // columns of a block
+      constexpr int JB = BC / JF;                                                // its tiles
+      constexpr int LPR = BC * (int)sizeof(T) / 16, RPI = 64 / LPR;              // lanes of a row, rows of a store
+      static_assert(JB >= 1 && BC % JF == 0 && WF % BC == 0);
       typedef T piece_t __attribute__((ext_vector_type(16 / sizeof(T))));
+      typedef T run_t __attribute__((ext_vector_type(4)));
       constexpr int PC = 16 / sizeof(T);                 // columns of a piece
       const int after = a.N - (bx + col) * BF - wn * WF;  // columns from the wavefront's first on
       const bool edge = after < WF;
-      int lo = li, ho = hh;
-      asm volatile("" : "+v"(lo), "+v"(ho));  // or the stores' offsets would all be kept over the column tiles
+      int lo = li, ho = hh, pl = lane % LPR, pr = lane / LPR;
+      asm volatile("" : "+v"(lo), "+v"(ho), "+v"(pl), "+v"(pr));  // or the stores' offsets would all be kept over the column tiles
       const float *sc = reinterpret_cast<const float *>(lds + S::SCALES) + (col & 1) * 2 * BN + wn * WF + 4 * ho;
+      uint8_t *block = lds + S::OUT + wv * S::OUT_WAVE;
 #pragma unroll
-      for (int j = 0; j < NI; j++) {
+      for (int i = 0; i < MX; i++) {
+        uint32_t off[32 / RPI];  // of this lane's pieces of a block: the row's start, or past the end
 #pragma unroll
-        for (int g = 0; g < GROUPS; g += sizeof(T) == 4 ? 1 : 2) {
-          constexpr int RUNS = sizeof(T) == 4 ? 1 : 2;
-          v4f cs[RUNS], cb[RUNS];  // of this lane's runs: scales, and the up rows' scales or biases
+        for (int k = 0; k < 32 / RPI; k++) {
+          const int row = wm * (BM / S::WM) + i * 32 + k * RPI + pr;
+          off[k] = row < n ? ((uint32_t)out_row(row) * (uint32_t)a.N + (bx + col) * BF + wn * WF) * sizeof(T) : ~0u;
+        }
 #pragma unroll
-          for (int d = 0; d < RUNS; d++) {
-            cs[d] = *reinterpret_cast<const v4f *>(sc + j * JF + 8 * (g + d));
-            if constexpr (MODE != I8_DOWN) cb[d] = *reinterpret_cast<const v4f *>(sc + BF + j * JF + 8 * (g + d));
-          }
+        for (int j0 = 0; j0 < NI; j0 += JB) {
 #pragma unroll
-          for (int i = 0; i < MX; i++) {
-            const int row = wm * (BM / S::WM) + i * 32 + lo;
-            const bool there = row < n;
-            const uint32_t off = ((uint32_t)out_row(row) * (uint32_t)a.N + (bx + col) * BF + wn * WF) * sizeof(T);
-            auto value = [&](int d, int r) -> T {
-              if constexpr (MODE == I8_GATEUP)
-                return (T)i8_product(i8_silu(i8_value(acc[i][j][8 * (g + d) + r], row_scale[i], cs[d][r])),
-                                     i8_value(acc[i][j][8 * (g + d) + 4 + r], row_scale[i], cb[d][r]));
-              else if constexpr (MODE == I8_LINEAR)
-                return (T)(i8_value(acc[i][j][4 * (g + d) + r], row_scale[i], cs[d][r]) + cb[d][r]);
-              else
-                return (T)i8_value(acc[i][j][4 * (g + d) + r], row_scale[i], cs[d][r]);
-            };
-            auto put = [&](piece_t w, int c) {
-              const uint32_t at = off + c * sizeof(T);
-              store_out(w, out, there && c + PC <= after ? at : ~0u);
-              if (RAGGED && __builtin_expect(edge, 0)) {
+          for (int jj = 0; jj < JB; jj++) {
+            const int j = j0 + jj;
 #pragma unroll
-                for (int r = 0; r < PC; r++)
-                  store_out(w[r], out, there && c + PC > after && c + r < after ? at + r * (int)sizeof(T) : ~0u);
+            for (int g = 0; g < GROUPS; g++) {
+              const v4f cs = *reinterpret_cast<const v4f *>(sc + j * JF + 8 * g);
+              v4f cb = {};
+              if constexpr (MODE != I8_DOWN) cb = *reinterpret_cast<const v4f *>(sc + BF + j * JF + 8 * g);
+              run_t w;
+#pragma unroll
+              for (int r = 0; r < 4; r++) {
+                if constexpr (MODE == I8_GATEUP)
+                  w[r] = (T)i8_product(i8_silu(i8_value(acc[i][j][8 * g + r], row_scale[i], cs[r])),
+                                       i8_value(acc[i][j][8 * g + 4 + r], row_scale[i], cb[r]));
+                else if constexpr (MODE == I8_LINEAR)
+                  w[r] = (T)(i8_value(acc[i][j][4 * g + r], row_scale[i], cs[r]) + cb[r]);
+                else
+                  w[r] = (T)i8_value(acc[i][j][4 * g + r], row_scale[i], cs[r]);
               }
-            };
-            if constexpr (sizeof(T) == 4) {
-              piece_t w;
-#pragma unroll
-              for (int r = 0; r < 4; r++) w[r] = value(0, r);
-              put(w, j * JF + 8 * g + 4 * ho);
-            } else {
-              typedef T half_t __attribute__((ext_vector_type(4)));
-              half_t x, y;
-#pragma unroll
-              for (int r = 0; r < 4; r++) x[r] = value(0, r), y[r] = value(1, r);
-              const v2u32 xu = __builtin_bit_cast(v2u32, x), yu = __builtin_bit_cast(v2u32, y);
-              // the lower lanes get their partner's run of g, the upper ones theirs of g + 1
-              const auto p = __builtin_amdgcn_permlane32_swap(xu[0], yu[0], false, false);
-              const auto q = __builtin_amdgcn_permlane32_swap(xu[1], yu[1], false, false);
-              put(__builtin_bit_cast(piece_t, v4u32{p[0], q[0], p[1], q[1]}), j * JF + 8 * (g + ho));
+              *reinterpret_cast<run_t *>(block + lo * S::OUT_ROW + (jj * JF + 8 * g + 4 * ho) * (int)sizeof(T)) = w;
+              __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
           }
+          // a wavefront's LDS accesses are done in order
+          __builtin_amdgcn_wave_barrier();
+          asm volatile("" ::: "memory");
+#pragma unroll
+          for (int k = 0; k < 32 / RPI; k++) {
+            const piece_t w = *reinterpret_cast<const piece_t *>(block + (k * RPI + pr) * S::OUT_ROW + pl * 16);
+            const int c = j0 * JF + pl * PC;
+            const bool there = off[k] != ~0u;
+            const uint32_t to = off[k] + c * (int)sizeof(T);
+            store_out(w, out, there && c + PC <= after ? to : ~0u);
+            if (RAGGED && __builtin_expect(edge, 0)) {
+#pragma unroll
+              for (int r = 0; r < PC; r++)
+                store_out(w[r], out, there && c + PC > after && c + r < after ? to + r * (int)sizeof(T) : ~0u);
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
@@ -322,15 +341,21 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
   // routed rows and short batches seldom fill a tile: the products of the 32-row tiles that hold
   // none are left out
   if constexpr (S::WM > 1) {
-    run.template operator()<MI>();
+    run.template operator()<MI, false>();
   } else {
     static_assert(MI == 4);
-    if (n <= 32)
-      run.template operator()<1>();
-    else if (n <= 64)
-      run.template operator()<2>();
+    auto rows = [&]<bool ONCE>() {
+      if (n <= 32)
+        run.template operator()<1, ONCE>();
+      else if (n <= 64)
+        run.template operator()<2, ONCE>();
+      else
+        run.template operator()<4, ONCE>();
+    };
+    if (MODE != I8_LINEAR && once)
+      rows.template operator()<MODE != I8_LINEAR>();
     else
-      run.template operator()<4>();
+      rows.template operator()<false>();
   }
 }
 
@@ -341,7 +366,7 @@ static hipError_t launch_tile(I8Args a, int ny, hipStream_t s) {
   auto kernel = i8_tile_kernel<MODE, T, S, RAGGED>;
   static PerDevice allowed;
   if (const hipError_t st = allow_lds(allowed, kernel, S::BYTES); st != hipSuccess) return st;
-  a.strip = MODE == I8_LINEAR ? dense_strip(a.N, BF, ny, MX_CUS * S::OCC) : 2;
+  a.strip = S::STRIPS ? dense_strip(a.N, BF, ny, MX_CUS * S::OCC) : 1;
   const unsigned groups = (unsigned)tile_strips(a.N, BF, a.strip) * (unsigned)ny;
   hipLaunchKernelGGL(kernel, dim3(MODE == I8_LINEAR ? groups : (groups + 7) / 8 * 8), dim3(256), S::BYTES, s, a);
   return hipGetLastError();

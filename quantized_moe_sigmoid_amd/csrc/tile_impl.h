@@ -26,6 +26,18 @@ __device__ __forceinline__ void dma16_pair(const uint8_t *base, uint32_t o0, uin
       : "s"(lds + 4096), "s"(lanes_of(lo, hi)), "v"(o0), "v"(o1), "s"(base)
       : "memory", "scc");
 }
+// The same, for what no other workgroup will read: past the caches
+__device__ __forceinline__ void dma16_pair_once(const uint8_t *base, uint32_t o0, uint32_t o1, uint32_t lds, int lo, int hi) {
+  uint64_t active;
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %1, m0\n\ts_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\t"
+      "global_load_lds_dwordx4 %4, %6 offset:-4096 nt\n\tglobal_load_lds_dwordx4 %5, %6 nt\n\t"
+      "s_mov_b32 m0, %1\n\ts_mov_b64 exec, %0"
+      : "=&s"(active), "=&s"(m0)
+      : "s"(lds + 4096), "s"(lanes_of(lo, hi)), "v"(o0), "v"(o1), "s"(base)
+      : "memory", "scc");
+}
 __device__ __forceinline__ void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int lo, int hi) {
   uint64_t active;
   uint32_t m0;

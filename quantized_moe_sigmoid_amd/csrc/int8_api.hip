@@ -74,18 +74,34 @@ static I8Args expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
   return a;
 }
 
-// A dense product on the tiled kernel?
+// A dense product on the tiled kernel? The kernel for few rows goes through the weights once for each
+// 64 rows (32 at half the time), a workgroup of the tiled one takes as long for one tile as for many.
+// us, few rows and tiled, K = 6144: N = 12288: 17 rows 28 and 36, 32 33 and 37, 64 49 and 37, 128 88
+// and 41; N = 2048: 64 rows 23 and 35, 256 36 and 41, 512 62 and 40. K = 2048: 32 x 40000 34 and 19,
+// 64 x 6144 17 and 17; 256 x 4096 x 1024 17 and 13; 128 x 4096 x 4096 25 and 27.
 static bool i8_linear_tiled(int32_t M, int32_t N) {
   if (M <= 16) return false;
-  return (M <= 32 ? 2 : (M + 63) / 64 * 4) * (int64_t)N > 40960;
+  return (M <= 32 ? 3 : (M + 63) / 64 * 4) * (int64_t)N > 38000;
+}
+
+// The kernel for few rows reads an expert's weights once for each 16 rows, the tiled one fills the card
+// with about four tiles to a CU and reads faster then. us, few rows and tiled, gate/up and down:
+//   256 experts of 6144 x 2048, 8 to a token: 24 tokens      606 and 636    307 and 320
+//     40 tokens                                              814 and 744    438 and 427
+//     64 tokens, and a shared one                            906 and 816    541 and 494
+//   64 of 2048 x 1024, 8 to a token: 32, 64 tokens           59, 57 and 60, 54   41, 45 and 46, 46
+//   32 of 1024 x 512: 300 tokens                             15 and 20      17 and 21
+//   8 of 4096 x 2048: 64, 128 tokens                         36, 48 and 36, 42   23, 30 and 29, 30
+//   8 of 6144 x 2048, 2 to a token: 200 tokens               140 and 66     92 and 41
+static bool i8_experts_tiled(const I8Args &a) {
+  const int64_t P = (int64_t)a.M * a.k, hit = std::min<int64_t>(P, a.E);
+  return P > 12 * (int64_t)a.E || (P > 256 && hit * a.N >= 1024 * 128);
 }
 
 static hipError_t launch_experts(I8Mode mode, int dtype, I8Args &a, uint8_t *ws, const I8Ws &L, hipStream_t s) {
-  // The kernel for few rows up to 512 pairs (decode batches), the tiled one past them; its offsets
-  // into the activations and the output have 32 bits.
+  // the tiled kernel's offsets into the activations and the output have 32 bits
   const int64_t rows = (int64_t)a.M * (a.k + a.has_shared), widest = std::max<int64_t>((int64_t)a.N * 4, i8_padded(a.K));
-  if ((int64_t)a.M * a.k <= LOCAL_GROUP_MAX_P || rows * widest >= ((int64_t)1 << 32) - 65536)
-    return launch_i8_gemv(mode, dtype, a, s);
+  if (!i8_experts_tiled(a) || rows * widest >= ((int64_t)1 << 32) - 65536) return launch_i8_gemv(mode, dtype, a, s);
   a.tiles = reinterpret_cast<int4 *>(ws + L.tiles);
   a.ntiles = reinterpret_cast<int32_t *>(ws + L.ntiles);
   return launch_i8_tile(mode, dtype, a, s);

@@ -324,7 +324,7 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
             const int c = j0 * JF + pl * PC;
             const bool there = off[k] != ~0u;
             const uint32_t to = off[k] + c * (int)sizeof(T);
-            store_out(w, out, there && c + PC <= after ? to : ~0u);
+            store_out<2>(w, out, there && c + PC <= after ? to : ~0u);
             if (RAGGED && __builtin_expect(edge, 0)) {
 #pragma unroll
               for (int r = 0; r < PC; r++)

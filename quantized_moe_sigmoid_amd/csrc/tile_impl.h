@@ -81,10 +81,11 @@ __device__ __forceinline__ void tile_of(int id, int nx, int ny, int &x, int &y) 
   x = strip * TILE_STRIP + in - y * w;
 }
 
-template <typename W>
+// AUX 2: 16-byte pieces pass the caches by
+template <int AUX = 0, typename W>
 __device__ __forceinline__ void store_out(W w, __amdgpu_buffer_rsrc_t out, uint32_t off) {
   if constexpr (sizeof(W) == 16)
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, w), out, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, w), out, off, 0, AUX);
   else if constexpr (sizeof(W) == 4)
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, w), out, off, 0, 0);
   else

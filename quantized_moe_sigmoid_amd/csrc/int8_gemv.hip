@@ -183,18 +183,18 @@ __global__ __launch_bounds__(256, ACT == I8_ACT_X || NT == 4 ? 2 : 4) void i8_ge
           arow = MODE == I8_DOWN ? orow : (routed ? orow / a.k : ci);
         }
         const float s = ACT == I8_ACT_X ? xs : a.as[arow];
-        auto value = [&](int m) {  // of the gate's or only matrix, of the up's
+        auto sum = [&](int m) {  // of the gate's or only matrix, of the up's
           const int i = HALVES ? 0 : m, c = HALVES ? tc + 8 * m : tc;
-          const int sum = red[0][i][q][tr][c] + red[1][i][q][tr][c] + red[2][i][q][tr][c] + red[3][i][q][tr][c];
-          return i8_value(sum, s, ws[(int64_t)m * a.N]);
+          return red[0][i][q][tr][c] + red[1][i][q][tr][c] + red[2][i][q][tr][c] + red[3][i][q][tr][c];
         };
+        auto value = [&](int m) { return i8_value(sum(m), s, ws[(int64_t)m * a.N]); };
         const int64_t o = orow * a.N + n0 + tc;
         if constexpr (MODE == I8_GATEUP)
           static_cast<T *>(a.out)[o] = (T)i8_product(i8_silu(value(0)), value(1));
         else if constexpr (MODE == I8_DOWN)
           static_cast<float *>(a.out)[o] = value(0);
         else
-          static_cast<T *>(a.out)[o] = (T)(value(0) + (a.bias ? a.bias[n0 + tc] : 0.0f));
+          static_cast<T *>(a.out)[o] = (T)i8_biased(sum(0), s, ws[0], a.bias ? a.bias[n0 + tc] : 0.0f);
       }
     }
     if (c + 16 * NT < n) __syncthreads();

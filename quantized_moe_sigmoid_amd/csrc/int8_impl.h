@@ -72,8 +72,13 @@ __device__ __forceinline__ float i8_product(float a, float b) {
   return y;
 }
 
-// y of an exact sum
+// y of an exact sum, and with a bias (likewise a value of its own)
 __device__ __forceinline__ float i8_value(int acc, float row, float channel) { return i8_product((float)acc, row * channel); }
+__device__ __forceinline__ float i8_biased(int acc, float row, float channel, float bias) {
+  float y = i8_value(acc, row, channel) + bias;
+  asm volatile("" : "+v"(y));
+  return y;
+}
 
 // silu(g) = g / (1 + e^-g) from t = e^-|g|, which does not overflow: g / (1 + t), or g t / (1 + t) below
 // 0, so that gates down to -103, where g t leaves fp32, count. t = 2^h (1 + l ln 2) with h + l =

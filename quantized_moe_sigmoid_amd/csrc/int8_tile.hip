@@ -307,7 +307,7 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
                   w[r] = (T)i8_product(i8_silu(i8_value(acc[i][j][8 * g + r], row_scale[i], cs[r])),
                                        i8_value(acc[i][j][8 * g + 4 + r], row_scale[i], cb[r]));
                 else if constexpr (MODE == I8_LINEAR)
-                  w[r] = (T)(i8_value(acc[i][j][4 * g + r], row_scale[i], cs[r]) + cb[r]);
+                  w[r] = (T)i8_biased(acc[i][j][4 * g + r], row_scale[i], cs[r], cb[r]);
                 else
                   w[r] = (T)i8_value(acc[i][j][4 * g + r], row_scale[i], cs[r]);
               }

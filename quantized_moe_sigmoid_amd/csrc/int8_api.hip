@@ -74,15 +74,11 @@ static I8Args expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
   return a;
 }
 
-// A dense product on the tiled kernel? The kernel for few rows goes through the weights once for each
-// 64 rows (32 at half the time), a workgroup of the tiled one takes as long for one tile as for many.
-// us, few rows and tiled, K = 6144: N = 12288: 17 rows 28 and 36, 32 33 and 37, 64 49 and 37, 128 88
-// and 41; N = 2048: 64 rows 23 and 35, 256 36 and 41, 512 62 and 40. K = 2048: 32 x 40000 34 and 19,
-// 64 x 6144 17 and 17; 256 x 4096 x 1024 17 and 13; 128 x 4096 x 4096 25 and 27.
-static bool i8_linear_tiled(int32_t M, int32_t N) {
-  if (M <= 16) return false;
-  return (M <= 32 ? 3 : (M + 63) / 64 * 4) * (int64_t)N > 38000;
-}
+// A dense product on the tiled kernels? The kernel for few rows goes through the weights once for each 64
+// rows. us, few rows and tiled, K = 6144: N = 12288: 2 rows 19 and 21, 4 20 and 21, 16 25 and 22, 64 49 and
+// 22; N = 2048: 16 rows 14 and 21, 33 19 and 21, 64 22 and 21; 200 x 512 22 and 21, 1000 x 128 25 and 23.
+// K = 2048: 16 x 6144 11 and 12, 16 x 40000 25 and 24, 33 x 512 12 and 12.
+static bool i8_linear_tiled(int32_t M, int32_t N) { return M > 48 || (M > 8 && (int64_t)M * N > 150000); }
 
 // The kernel for few rows reads an expert's weights once for each 16 rows, the tiled one fills the card
 // with about four tiles to a CU and reads faster then. us, few rows and tiled, gate/up and down:

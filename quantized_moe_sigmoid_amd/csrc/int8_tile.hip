@@ -31,6 +31,8 @@ struct I8Shape {
 };
 typedef I8Shape<256, 256, 2, 2, 2, 1, true> I8Dense;
 typedef I8Shape<128, 128, 1, 4, 2, 2, false> I8DenseSmall;
+typedef I8Shape<128, 64, 2, 2, 3, 2, false> I8DenseNarrow;
+typedef I8Shape<64, 64, 2, 2, 4, 2, false> I8DenseTiny;
 typedef I8Shape<128, 256, 1, 4, 3, 1, false> I8Experts;
 
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -372,8 +374,12 @@ static hipError_t launch_tile(I8Args a, int ny, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Fewer big tiles than this leave too many CUs without work.
-constexpr int DENSE_BIG_TILES = 192;
+// Tiles of a dense product, by how many there are of the next smaller kind: as large as fill the card.
+// us with 64 x 64, 128 x 64, 128 x 128 tiles: 64 x 12288 x 6144 (192 tiles of 64 x 64) 22, 25, 37;
+// 1000 x 1024 x 4096 (256) 18, 21, 29; 128 x 12288 x 6144 (384) 28, 26, 41; 1000 x 2048 x 6144 (512) 32,
+// 30, 42; 256 x 12288 x 6144 (768) 51, 46, 47-51; 1000 x 4096 x 4096 (1024) 39, 31, 32; 500 x 12288 x 6144
+// (1536) 71-76, 58, 51-58; 2000 x 4096 x 4096 (2048) 72, 55, 48.
+constexpr int64_t DENSE_TINY_TILES = 256, DENSE_NARROW_TILES = 1024, DENSE_BIG_TILES = 192;
 
 int64_t i8_tile_cap(int32_t T, int32_t k, int32_t E, int32_t has_shared) {
   const int64_t P = (int64_t)T * k, bm = I8Experts::BM;
@@ -388,8 +394,11 @@ static hipError_t launch_tile_t(I8Mode mode, const I8Args &a, hipStream_t s) {
       return a.N % (16 / sizeof(T)) == 0 ? launch_tile<I8_LINEAR, T, S>(a, ny, s)
                                          : launch_tile<I8_LINEAR, T, S, true>(a, ny, s);
     };
-    const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-    return tiles >= DENSE_BIG_TILES ? go.template operator()<I8Dense>() : go.template operator()<I8DenseSmall>();
+    const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+    const int64_t tiny = (int64_t)((a.M + 63) / 64) * ((a.N + 63) / 64);
+    if (big >= DENSE_BIG_TILES) return go.template operator()<I8Dense>();
+    if (tiny <= DENSE_TINY_TILES) return go.template operator()<I8DenseTiny>();
+    return tiny <= DENSE_NARROW_TILES ? go.template operator()<I8DenseNarrow>() : go.template operator()<I8DenseSmall>();
   }
   const int cap = (int)i8_tile_cap(a.M, a.k, a.E, a.has_shared);
   hipLaunchKernelGGL(route_tiles_kernel<I8Args>, dim3(1), dim3(1024), 0, s, a, I8Experts::BM, cap);

@@ -161,7 +161,9 @@ LINEAR = [(1, 1, 16), (1, 16, 64), (1, 77, 2064), (1, 300, 6144), (1, 5, 49168),
           (17, 31, 1040), (33, 129, 528), (64, 48, 2048), (65, 130, 4112), (200, 77, 784), (7, 2051, 144), (129, 1, 48),
           (300, 515, 1008), (513, 1031, 320), (1000, 257, 2064), (257, 256, 16), (770, 520, 112), (512, 512, 8192),
           (20, 20500, 48), (70, 5200, 272), (300, 2051, 1008), (1000, 1031, 2064), (129, 3460, 16), (513, 4096, 8192), (2900, 4100, 144),
-          (3001, 4361, 400), (3000, 4096, 1024), (257, 49160, 16), (32, 12700, 80), (64, 9510, 656), (512, 1200, 528)]
+          (3001, 4361, 400), (3000, 4096, 1024), (257, 49160, 16), (32, 12700, 80), (64, 9510, 656), (512, 1200, 528),
+          (1500, 3001, 272), (1300, 4096, 1040), (1601, 3090, 144), (48, 3125, 1296), (48, 3126, 1296), (49, 63, 400), (9, 17000, 640),
+          (8, 19000, 640), (1025, 1023, 7200)]
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -180,7 +182,7 @@ def test_linear_exact(q, dtype, M, N, K):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("M,N,K", [(1, 300, 2064), (7, 77, 528), (65, 130, 4112), (515, 1027, 272), (300, 768, 1024), (515, 4099, 272),
-                                   (2900, 4352, 528)])
+                                   (2900, 4352, 528), (1500, 3001, 272), (130, 8000, 1040), (61, 190, 2064)])
 def test_linear_bias(q, dtype, M, N, K):
     rng = np.random.default_rng(M + N + K)
     x = _rows(rng, M, K, dtype)

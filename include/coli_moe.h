@@ -303,7 +303,8 @@ int coli_moe_mxfp4_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, cons
  *   rounded to nearest, halves away from zero, clamped to [-127, 127]; s = 0 gives q = 0. A row
  *   that holds an infinity or a NaN has s = NaN and codes 0.
  * acc = sum_k q_k w_k is exact (int32); a product is (float)acc * (s_row * s_channel), so that it
- * depends neither on the batch nor on the kernel that a size takes. Outputs are rounded once. */
+ * depends neither on the batch nor on the kernel that a size takes. Outputs are rounded once.
+ * A workspace is used by one call at a time: calls that may overlap (other streams) need their own. */
 
 /* int8 of rows x cols values (cols % 16 == 0, cols <= 2^17; x and codes 16-byte aligned): codes
  * [rows][cols], scales fp32 [rows]. rows < 2^31, rows * cols < 2^40. */

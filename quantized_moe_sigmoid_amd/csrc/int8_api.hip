@@ -81,17 +81,19 @@ static I8Args expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
 static bool i8_linear_tiled(int32_t M, int32_t N) { return M > 48 || (M > 8 && (int64_t)M * N > 150000); }
 
 // The kernel for few rows reads an expert's weights once for each 16 rows, the tiled one fills the card
-// with about four tiles to a CU and reads faster then. us, few rows and tiled, gate/up and down:
-//   256 experts of 6144 x 2048, 8 to a token: 24 tokens      606 and 636    307 and 320
-//     40 tokens                                              814 and 744    438 and 427
-//     64 tokens, and a shared one                            906 and 816    541 and 494
-//   64 of 2048 x 1024, 8 to a token: 32, 64 tokens           59, 57 and 60, 54   41, 45 and 46, 46
-//   32 of 1024 x 512: 300 tokens                             15 and 20      17 and 21
-//   8 of 4096 x 2048: 64, 128 tokens                         36, 48 and 36, 42   23, 30 and 29, 30
+// with about eight tiles to a CU and reads faster then. us, few rows and tiled, gate/up and down:
+//   256 experts of 6144 x 2048, 8 to a token, and a shared one:
+//     17 tokens                                              483 and 447    253 and 257
+//     24 tokens                                              547 and 516    316 and 304
+//     64 tokens                                              1015 and 903   543 and 512
+//   64 of 2048 x 1024, 8 to a token: 17, 64, 200 tokens      48, 57, 104 and 49, 56, 57   37, 43, 75 and 43, 48, 52
+//   32 of 1024 x 512: 300 tokens                             15 and 20      15 and 20
+//   8 of 4096 x 2048: 64, 128 tokens                         36, 48 and 38, 42   23, 30 and 29, 30
 //   8 of 6144 x 2048, 2 to a token: 200 tokens               140 and 66     92 and 41
+// (64 x 64 and 64 x 128 tiles over a route: slower than either but for 600 tokens over 32 of 1024 x 512, 24 and 26.)
 static bool i8_experts_tiled(const I8Args &a) {
   const int64_t P = (int64_t)a.M * a.k, hit = std::min<int64_t>(P, a.E);
-  return P > 12 * (int64_t)a.E || (P > 256 && hit * a.N >= 1024 * 128);
+  return P > 12 * (int64_t)a.E || (P > 128 && hit * a.N >= 2048 * 128);
 }
 
 static hipError_t launch_experts(I8Mode mode, int dtype, I8Args &a, uint8_t *ws, const I8Ws &L, hipStream_t s) {

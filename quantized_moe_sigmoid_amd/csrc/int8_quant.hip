@@ -2,6 +2,8 @@
 //
 // Bound by memory: a value is read once and a byte of it written. Rows up to 8192 values stay in
 // registers between the search for their largest magnitude and the rounding; longer rows are read twice.
+// 18432 x 2048 fp32 31 us (6.0 TB/s), 14745 x 2048 bf16 20 (4.6), 4093 x 6144 bf16 19 (4.0). Pieces of 8
+// values a lane: 23, 32 and 19.5; a wavefront to a row of 6144: 25.
 #include "int8_impl.h"
 
 namespace coli {

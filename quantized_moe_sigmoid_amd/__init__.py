@@ -724,6 +724,8 @@ def combine_backward(dout, rows, pos, topk_w, drows=None, dtopk_w=None, stream=N
     d = _elem(dout, "dout")
     k = _slots(pos, T, "dout")
     f32 = _ELEM["f32"]
+    if rows is None and dtopk_w is not None:
+        raise ValueError("rows: dtopk_w needs combine's rows")
     some = drows if rows is None else rows
     R = 0 if some is None else some.shape[0]
     _run("coli_moe_combine_backward", dev, stream, _arg(dout, dt, None, dev, "dout"),

@@ -153,6 +153,7 @@ def test_binding_checks(q):
                  lambda: q.dispatch(f(2, 32), i(4), f(4, 32)), lambda: q.combine(f(4, 32), i(4), f(2, 32)),
                  lambda: q.combine(f(4, 32), i(5), f(2, 32)), lambda: q.dispatch(f(2, 32), i(3), f(4, 32)),  # no whole slots
                  lambda: q.combine_backward(f(2, 32), f(4, 32), i(4), f(2, 2), f(4, 32), f(2, 2)),
+                 lambda: q.combine_backward(f(2, 32), None, i(4), f(2, 2), None, f(2, 2)),
                  lambda: q.route_logits_backward(q.make_router(16, 2), f(3, 16), i(3, 2), f(3, 2), f(3, 16))):
         with pytest.raises(ValueError):
             call()

@@ -13,8 +13,6 @@
 //
 // i8_down_kernel: 16 tokens over 256 experts of 6144 x 2048 232 us (1.29 GB, 5.6 TB/s with the quantisation's
 // launch), one token 24 (113 MB; a bare read of them in this order takes 18.6).
-#include <cmath>
-
 #include "int8_impl.h"
 
 namespace coli {
@@ -226,13 +224,12 @@ __host__ __device__ inline I8DownLds i8_down_lds(const I8Args &a, int step, int 
   return L;
 }
 
-// The down product of up to 16 tokens with its weighted combine. A workgroup (8
-// wavefronts) owns `step` output rows, RT 16-row tiles of the matrix instruction, and goes through all
-// experts that its tokens hold, a token to a column; rows past them, like rows past N, read past their
-// buffer's end, which gives zeros without an access. 1 << lp wavefronts share an expert's K groups; what
-// each sums for a (token, slot) has its own place in LDS, and at the end the parts, then the weighted
-// slots, then the shared expert's row are added in order: a token's row does not depend on the tokens
-// beside it.
+// The down product of up to 16 tokens with its weighted combine. A workgroup (8 wavefronts) owns `step` output
+// rows, RT 16-row tiles of the matrix instruction, and goes through all experts that its tokens hold, a token to a
+// column; rows past them, like rows past N, read past their buffer's end, which gives zeros without an access. 1 <<
+// lp wavefronts share an expert's K groups; what each sums for a (token, slot) has its own place in LDS, and at the
+// end the parts, then the weighted slots, then the shared expert's row are added in order: a token's row does not
+// depend on the tokens beside it.
 template <typename T, I8Act ACT, int RT>
 __global__ __launch_bounds__(64 * DN_WAVES) void i8_down_kernel(I8Args a, int step, int lp, const int32_t *__restrict__ idx,
                                                                const float *__restrict__ w, T *__restrict__ out) {
@@ -411,9 +408,7 @@ __global__ __launch_bounds__(64 * DN_WAVES) void i8_down_kernel(I8Args a, int st
 #pragma unroll
     for (int q = 0; q < DN_XP; q++) {
       const int u = tid + 64 * DN_WAVES * q, r = u / per;
-      if (u < n) {
-        *reinterpret_cast<uint2 *>(lx + r * pitch + (u - r * per) * 8) = i8_codes8(xv[q], i8_row(tops[r]));
-      }
+      if (u < n) *reinterpret_cast<uint2 *>(lx + r * pitch + (u - r * per) * 8) = i8_codes8(xv[q], i8_row(tops[r]));
     }
     for (int i = tid; i < ks * (pitch / 8 - per); i += 64 * DN_WAVES) {  // up to 16 pieces a row
       const int r = i / (pitch / 8 - per);

@@ -139,6 +139,20 @@ def test_quantise_not_finite(q, dtype, cols):
     assert np.array_equal(codes, rc)
 
 
+def test_quantise_more_rows_than_one_launch(q):
+    import torch
+    rows = 8 * (1 << 23) + 9
+    x = torch.zeros((rows, 16), dtype=torch.bfloat16, device="cuda")
+    at = [0, 1 << 26, rows - 10, rows - 9, rows - 1]
+    for i in at:
+        x[i] = torch.randn(16, device="cuda")
+    codes, scales = torch.full((rows, 16), 5, dtype=torch.int8, device="cuda"), torch.full((rows,), 5.0, device="cuda")
+    q.int8_quantize(x, codes, scales)
+    rc, rs = i8ref.quantise(x[at].float().cpu().numpy())
+    assert np.array_equal(codes[at].cpu().numpy(), rc) and np.array_equal(scales[at].cpu().numpy(), rs)
+    assert int((codes != 0).any(1).sum()) == len(set(at)) and int((scales != 0).sum()) == len(set(at))
+
+
 # ------------------------------------------------------------------ dense product
 def _weights(rng, N, K):
     return (rng.integers(-128, 128, (N, K), dtype=np.int8),

@@ -288,3 +288,29 @@ def test_rows_past_32_bits(q):
     assert torch.allclose(dw, (x.float() ** 2).sum(1, keepdim=True).expand(T, k), rtol=H * U, atol=0)
     q.combine_backward(out, None, pos, w, dys)
     assert torch.equal(rows[pos.long()], (x / 2).repeat_interleave(k, 0))
+
+
+def test_more_elements_than_one_launch(q):
+    """Rows of no whole pieces with more than 2^32 elements, and more pairs than a launch has wavefronts for."""
+    import torch
+    T, H = 131073, 32769
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(0)
+    at = [0, 65535, 65536, T - 2, T - 1]
+    for i in at:
+        x[i] = _t(rng.standard_normal(H).astype(np.float32), "bfloat16")
+    pos = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    pos[at] = torch.arange(len(at), dtype=torch.int32, device="cuda").flip(0)
+    rows = torch.full((len(at) + 1, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    q.dispatch(x, pos, rows)
+    assert torch.equal(rows[:-1], x[at].flip(0)) and (rows[-1] == 3).all()
+    out = torch.full_like(x, 3.0)
+    q.combine(rows, pos, out)
+    assert torch.equal(out, x)
+    del x, out
+    P = 4 * (1 << 23) + 5
+    pos = torch.arange(P, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    y, w = torch.randn((P, 1), device="cuda"), torch.randn((P, 1), device="cuda")
+    dout, dy, dw = torch.randn((P, 1), device="cuda"), torch.empty((P, 1), device="cuda"), torch.empty((P, 1), device="cuda")
+    q.combine_backward(dout, y, pos, w, dy, dw)
+    assert torch.equal(dw, dout * y.flip(0)) and torch.equal(dy.flip(0), dout * w)

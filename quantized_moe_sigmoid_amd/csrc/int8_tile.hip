@@ -11,7 +11,7 @@
 // fills the accumulators; a row of a stage is one 128-byte line.
 //
 // Over a route, 2048 tokens, 256 experts of 6144 x 2048 and a shared one, Zipf-like: gate/up 1268 to 1300
-// us, down 745 (and 82 for the combine, 20 for the quantisation of h). Bound by the weights' way from HBM:
+// us, down 745 (and 78 for the combine, 20 for the quantisation of h). Bound by the weights' way from HBM:
 // without products or LDS reads the same. Column strips of 1, 2 and 4 tiles 1344, 1381 and 1459 us;
 // weights that one row tile alone reads past the caches 1344 -> 1300 (all weights: 1344, row tiles that share
 // them meet in the L2); results past the caches 1307 -> 1283.

@@ -593,28 +593,45 @@ hipError_t launch_mx_down(const MxArgs &a, const int32_t *idx, const float *w, v
   return launch_down_t<f16_t>(a, idx, w, out, s);
 }
 
-// out_t = sum_j w_tj y_tj in slot order, plus the shared expert's row; empty slots skipped
+// out_t = sum_j w_tj y_tj in slot order, plus the shared expert's row; empty slots skipped. Four columns of a
+// token to a thread, the rows of eight slots under way at a time; they are used once and pass the caches by. Down
+// products of 2048 tokens with 8 slots and a shared expert, H = 6144: MXFP4 584 us (a slot after another,
+// through the caches: 595), int8 829 (834; through the caches 832, four slots at a time 830).
 template <typename T>
 __global__ __launch_bounds__(256) void mx_combine_kernel(const float *__restrict__ y, const int32_t *__restrict__ idx,
                                                          const float *__restrict__ w, int T_, int k, int E, int H,
                                                          int has_shared, T *__restrict__ out) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  const int64_t t = i / H;
-  const int h = (int)(i - t * H);
-  if (t >= T_) return;
-  v4f s = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < k; j++) {
-    const int64_t p = t * k + j;
-    const int e = idx[p];
-    if (e < 0 || e >= E) continue;
-    s += w[p] * *reinterpret_cast<const v4f *>(y + p * H + h);
+  constexpr int AHEAD = 8;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x, per = (uint32_t)H / 4;  // T k < 2^16: fewer than 2^32
+  const uint32_t t = i / per, h = i - t * per;
+  if (t >= (uint32_t)T_) return;
+  const v4f *py = reinterpret_cast<const v4f *>(y) + h;
+  v4f s = {0.f, 0.f, 0.f, 0.f}, last = s;
+  if (has_shared) last = __builtin_nontemporal_load(py + ((int64_t)T_ * k + t) * per);
+  for (int j0 = 0; j0 < k; j0 += AHEAD) {
+    v4f v[AHEAD];
+    bool there[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; j++) {
+      const int64_t p = (int64_t)t * k + j0 + j;
+      const int e = j0 + j < k ? idx[p] : -1;
+      there[j] = e >= 0 && e < E;
+      if (there[j]) v[j] = __builtin_nontemporal_load(py + p * per);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; j++) {
+      if (!there[j]) continue;
+      const float wt = w[(int64_t)t * k + j0 + j];
+#pragma unroll
+      for (int r = 0; r < 4; r++) s[r] = __builtin_fmaf(wt, v[j][r], s[r]);
+    }
   }
-  if (has_shared) s += *reinterpret_cast<const v4f *>(y + ((int64_t)T_ * k + t) * H + h);
+  if (has_shared) s += last;
   typedef T v4 __attribute__((ext_vector_type(4)));
   v4 o;
 #pragma unroll
   for (int r = 0; r < 4; r++) o[r] = (T)s[r];
-  *reinterpret_cast<v4 *>(out + i) = o;
+  *reinterpret_cast<v4 *>(out + (int64_t)i * 4) = o;
 }
 
 hipError_t launch_mx_combine(const float *y, const int32_t *idx, const float *w, int T, int k, int E, int H,

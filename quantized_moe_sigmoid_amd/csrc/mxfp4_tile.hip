@@ -14,7 +14,7 @@
 // 256 inputs, one row of a stage to a line. A wavefront's 128 x 128 part fills the accumulators.
 //
 // Over a route, 2048 tokens, 256 experts of 6144 x 2048, Zipf-like: gate/up 815 us, down 480 (and
-// 96 for the combine). Bound by the weights' way from HBM: 3.4 GB, of which the kernel fetches
+// 85 for the combine). Bound by the weights' way from HBM: 3.4 GB, of which the kernel fetches
 // 3.9 (a line of scale bytes comes back for every two stages). Measured when the whole took 825:
 // without products 804, without scales 749; 8 wavefronts to the tile 851 (with two stages in LDS
 // instead of three 960), two workgroups of 128 x 128 tiles to a CU 857; column strips of 1, 2, 3

@@ -343,14 +343,15 @@ int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const
  *     (0 if invalid), 256-byte aligned, enough for fewer pairs too.
  *   dispatch: xs [rows][H], row pair_pos[t k + j] = x row t, bit for bit. x [T][H].
  *   combine: out [T][H], out_t = sum_j w_tj ys[pair_pos[t k + j]] in slot order + add_t, in fp32 and
- *     rounded once. topk_w fp32 [T][k] or NULL (weights 1), add [T][H] or NULL. Without weights
- *     it is the gradient of dispatch; dispatch is the gradient of combine without weights.
+ *     rounded once. topk_w fp32 [T][k] or NULL (weights 1), add [T][H], which may be out, or
+ *     NULL. Without weights it is the gradient of dispatch; dispatch is the gradient of combine without
+ *     weights.
  *   combine_backward: from dout [T][H] and the ys of combine: dys [rows][H], row pair_pos[t k + j] =
  *     w_tj dout_t, and dtopk_w fp32 [T][k], w_tj's gradient <dout_t, ys row> summed in fp32 (0 for an
  *     empty slot). dys or dtopk_w may be NULL: not wanted. ys may be NULL without dtopk_w.
  * A place outside [0, rows) is an empty slot; rows that no pair has are not written (so rows may be
  * more than the pairs). A place may stand once. xs, ys, x, out, add, dout and dys of one dtype, any H,
- * aligned to their type (16 bytes and H a multiple of 16 bytes run faster); T k < 2^30, T H < 2^40. */
+ * aligned to their type (rows of whole aligned 16 bytes run fastest); T k < 2^30, T H < 2^40. */
 size_t coli_moe_sort_pairs_workspace_bytes(int64_t P, int32_t n_experts);
 int coli_moe_sort_pairs(const int32_t *topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t *expert_off,
                         int32_t *pair_perm, int32_t *pair_pos, int32_t *active, int32_t *n_active, void *workspace,

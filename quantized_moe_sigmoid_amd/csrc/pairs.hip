@@ -3,6 +3,8 @@
 //
 // All bound by memory: a row is read once for each use and written once. Sums are fp32 in slot order,
 // without atomics.
+#include <type_traits>
+
 #include "mxfp4_impl.h"
 
 namespace coli {
@@ -169,11 +171,15 @@ hipError_t launch_sort_pairs(SortArgs a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------ rows
-// A thread takes one piece (16 bytes, or one element where rows are not whole aligned pieces) of a
-// token's row, for all of its slots. Rows of pairs are used once and pass the caches by.
+// A thread takes one piece (16 bytes at any element's address; one element of rows shorter than that) of a
+// token's row, for all of its slots. SHIFT: rows are no whole pieces, and the last one is moved back to end
+// with its row. Rows of pairs are used once and pass the caches by.
+// With rows of no whole pieces taken by element, 4095 tokens, 8 slots, 2047 bf16: combine 152 us, its gradient
+// 141, in pieces 36 and 80.
 template <typename T, int VEC>
 struct VecOf {
-  typedef T type __attribute__((ext_vector_type(VEC)));
+  typedef T vec __attribute__((ext_vector_type(VEC)));
+  typedef vec type __attribute__((aligned(sizeof(T))));
 };
 template <typename T>
 struct VecOf<T, 1> {
@@ -181,6 +187,14 @@ struct VecOf<T, 1> {
 };
 template <typename T, int VEC>
 using piece_of = typename VecOf<T, VEC>::type;
+
+// Piece u of the row at p of H elements
+template <typename T, int VEC, bool SHIFT, typename Q>
+__device__ __forceinline__ auto piece_at(Q *p, uint32_t u, uint32_t H) {
+  const uint32_t at = SHIFT ? min(u * VEC, H - VEC) : u * VEC;
+  if constexpr (std::is_const_v<Q>) return reinterpret_cast<const piece_of<T, VEC> *>(p + at);
+  else return reinterpret_cast<piece_of<T, VEC> *>(p + at);
+}
 
 template <typename T, int VEC>
 __device__ __forceinline__ T part(const piece_of<T, VEC> &x, int e) {
@@ -209,36 +223,39 @@ __device__ __forceinline__ void split(int64_t i, uint32_t units, int64_t &row, u
 constexpr int SLOTS = 8;  // rows of a token under way at a time (combine of 2048 x 8 rows of 6144: 4: 42.5 us, 8: 41)
 
 // 8191 tokens, 8 slots, 2048 bf16: 50 us, 268 MB written at 5.4 TB/s. By pair, x read eight times through
-// the L2s of other XCDs: 73.
-template <typename U, bool WIDE>
-__global__ __launch_bounds__(256) void dispatch_kernel(const U *__restrict__ x, uint32_t T_, int k, uint32_t units,
+// the L2s of other XCDs: 73. Rows of no whole pieces meet in lines, which the L2 puts together: 6915 tokens, 8
+// slots, 406 fp32, with the sort 29 us, past the caches 36, by element 41.
+template <typename T, int VEC, bool SHIFT, bool WIDE>
+__global__ __launch_bounds__(256) void dispatch_kernel(const T *__restrict__ x, uint32_t T_, int k, uint32_t H, uint32_t units,
                                                        const int32_t *__restrict__ pos, int64_t rows,
-                                                       U *__restrict__ xs) {
+                                                       T *__restrict__ xs) {
   const int64_t n = (int64_t)T_ * units, step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
     int64_t t;
     uint32_t u;
     split<WIDE>(i, units, t, u);
-    const U v = x[i];
+    const piece_of<T, VEC> v = *piece_at<T, VEC, SHIFT>(x + t * H, u, H);
     for (int j0 = 0; j0 < k; j0 += SLOTS) {
       int64_t r[SLOTS];
 #pragma unroll
       for (int j = 0; j < SLOTS; j++) r[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
 #pragma unroll
       for (int j = 0; j < SLOTS; j++)
-        if (r[j] >= 0 && r[j] < rows) __builtin_nontemporal_store(v, xs + r[j] * units + u);
+        if (r[j] >= 0 && r[j] < rows) {
+          auto *to = piece_at<T, VEC, SHIFT>(xs + r[j] * H, u, H);
+          if constexpr (SHIFT) *to = v;
+          else __builtin_nontemporal_store(v, to);
+        }
     }
   }
 }
 
 // 2048 tokens, 8 slots of which a fifth is empty, 6144 fp16, a row added: 40 us, 211 MB at 5.3 TB/s; row loads
-// that fill the caches 49, empty slots' loads sent to row 0 instead of left out 41.
-template <typename T, int VEC, bool WIDE>
-__global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC> *__restrict__ ys, int64_t rows, uint32_t T_,
-                                                           int k, uint32_t units, const int32_t *__restrict__ pos,
-                                                           const float *__restrict__ w,
-                                                           const piece_of<T, VEC> *__restrict__ add,
-                                                           piece_of<T, VEC> *__restrict__ out) {
+// that fill the caches 49, empty slots' loads sent to row 0 instead of left out 41. add may be out.
+template <typename T, int VEC, bool SHIFT, bool WIDE>
+__global__ __launch_bounds__(256) void pair_combine_kernel(const T *__restrict__ ys, int64_t rows, uint32_t T_, int k, uint32_t H,
+                                                           uint32_t units, const int32_t *__restrict__ pos,
+                                                           const float *__restrict__ w, const T *add, T *out) {
   typedef piece_of<T, VEC> piece;
   const int64_t n = (int64_t)T_ * units, step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
@@ -253,7 +270,7 @@ __global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC
       for (int j = 0; j < SLOTS; j++) {
         const int64_t r = j0 + j < k ? pos[t * k + j0 + j] : -1;
         there[j] = r >= 0 && r < rows;
-        if (there[j]) y[j] = __builtin_nontemporal_load(ys + r * units + u);
+        if (there[j]) y[j] = __builtin_nontemporal_load(piece_at<T, VEC, SHIFT>(ys + r * H, u, H));
       }
 #pragma unroll
       for (int j = 0; j < SLOTS; j++) {
@@ -264,26 +281,32 @@ __global__ __launch_bounds__(256) void pair_combine_kernel(const piece_of<T, VEC
       }
     }
     if (add) {
-      const piece y = add[i];
+      const piece y = *piece_at<T, VEC, SHIFT>(add + t * H, u, H);
 #pragma unroll
       for (int e = 0; e < VEC; e++) s[e] += (float)part<T, VEC>(y, e);
     }
     piece o;
 #pragma unroll
     for (int e = 0; e < VEC; e++) set_part<T, VEC>(o, e, (T)s[e]);
-    __builtin_nontemporal_store(o, out + i);
+    T *po = out + t * H;
+    if (SHIFT && u == units - 1) {  // the elements before u VEC are another thread's, and add may be out
+#pragma unroll
+      for (int e = 0; e < VEC; e++)
+        if (H - VEC + e >= u * VEC) po[H - VEC + e] = part<T, VEC>(o, e);
+    } else {
+      __builtin_nontemporal_store(o, piece_at<T, VEC, SHIFT>(po, u, H));
+    }
   }
 }
 
 // A wavefront takes a pair: its row of the gradient, and the weight's. 4093 tokens, 8 slots, 2048 fp32: 102
 // us, 570 MB at 5.6 TB/s.
 constexpr int GRAD_AHEAD = 8;  // pieces of a lane under way: 2, 4, 8, 16: 126, 114, 104, 443 us
-template <typename T, int VEC>
-__global__ __launch_bounds__(256) void combine_grad_kernel(const piece_of<T, VEC> *__restrict__ dout,
-                                                           const piece_of<T, VEC> *__restrict__ ys, int64_t rows, uint32_t P,
-                                                           int k, uint32_t units, const int32_t *__restrict__ pos,
-                                                           const float *__restrict__ w, piece_of<T, VEC> *__restrict__ dys,
-                                                           float *__restrict__ dw) {
+template <typename T, int VEC, bool SHIFT>
+__global__ __launch_bounds__(256) void combine_grad_kernel(const T *__restrict__ dout, const T *__restrict__ ys, int64_t rows,
+                                                           uint32_t P, int k, uint32_t H, uint32_t units,
+                                                           const int32_t *__restrict__ pos, const float *__restrict__ w,
+                                                           T *__restrict__ dys, float *__restrict__ dw) {
   typedef piece_of<T, VEC> piece;
   const int lane = threadIdx.x & 63;
   for (uint32_t p = blockIdx.x * 4 + (threadIdx.x >> 6); p < P; p += gridDim.x * 4) {
@@ -291,14 +314,14 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const piece_of<T, VEC
     float sum = 0.0f;
     if (r >= 0 && r < rows) {
       const float wt = w[p];
-      const piece *d = dout + (int64_t)(p / k) * units, *yr = ys + r * units;
+      const T *d = dout + (int64_t)(p / k) * H, *yr = ys + r * H;
       for (uint32_t u0 = lane; u0 < units; u0 += 64 * GRAD_AHEAD) {
         piece g[GRAD_AHEAD], y[GRAD_AHEAD];
 #pragma unroll
         for (int a = 0; a < GRAD_AHEAD; a++) {
           const uint32_t u = min(u0 + 64 * a, units - 1);
-          g[a] = d[u];
-          if (dw) y[a] = __builtin_nontemporal_load(yr + u);
+          g[a] = *piece_at<T, VEC, SHIFT>(d, u, H);
+          if (dw) y[a] = __builtin_nontemporal_load(piece_at<T, VEC, SHIFT>(yr, u, H));
         }
 #pragma unroll
         for (int a = 0; a < GRAD_AHEAD; a++) {
@@ -306,13 +329,16 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const piece_of<T, VEC
           if (u >= units) break;
           if (dw) {
 #pragma unroll
-            for (int e = 0; e < VEC; e++) sum = __builtin_fmaf((float)part<T, VEC>(g[a], e), (float)part<T, VEC>(y[a], e), sum);
+            for (int e = 0; e < VEC; e++) {
+              const float more = __builtin_fmaf((float)part<T, VEC>(g[a], e), (float)part<T, VEC>(y[a], e), sum);
+              sum = !SHIFT || u < units - 1 || H - VEC + e >= u * VEC ? more : sum;  // each element once
+            }
           }
           if (dys) {
             piece o;
 #pragma unroll
             for (int e = 0; e < VEC; e++) set_part<T, VEC>(o, e, (T)(wt * (float)part<T, VEC>(g[a], e)));
-            __builtin_nontemporal_store(o, dys + r * units + u);
+            __builtin_nontemporal_store(o, piece_at<T, VEC, SHIFT>(dys + r * H, u, H));
           }
         }
       }
@@ -328,36 +354,40 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const piece_of<T, VEC
 // Workgroups of a launch of 256 threads each, fewer than 2^32 threads; the kernels loop over more
 static unsigned groups_of(int64_t n) { return (unsigned)(n < (1 << 23) ? n : (1 << 23)); }
 
-static bool whole(int H, int size, const void *a, const void *b, const void *c = nullptr) {
-  return (int64_t)H * size % 16 == 0 && (uintptr_t)a % 16 == 0 && (uintptr_t)b % 16 == 0 && (uintptr_t)c % 16 == 0;
+// Rows of H elements of T: go<pieces' elements, whether rows are no whole pieces>()
+template <typename T>
+static hipError_t by_row(int H, auto go) {
+  constexpr int VEC = 16 / sizeof(T);
+  if (H < VEC) return go.template operator()<1, false>();
+  return H % VEC ? go.template operator()<VEC, true>() : go.template operator()<VEC, false>();
+}
+
+template <typename T>
+static hipError_t launch_dispatch_t(const PairArgs &a, const T *x, T *xs, hipStream_t s) {
+  return by_row<T>(a.H, [&]<int VEC, bool SHIFT>() {
+    const uint32_t H = a.H, units = (H + VEC - 1) / VEC;
+    const int64_t n = (int64_t)a.T * units;
+    auto kernel = n < ((int64_t)1 << 32) ? dispatch_kernel<T, VEC, SHIFT, false> : dispatch_kernel<T, VEC, SHIFT, true>;
+    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, x, (uint32_t)a.T, a.k, H, units, a.pos, a.rows, xs);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_dispatch(const PairArgs &a, int dtype, const void *x, void *xs, hipStream_t s) {
-  const int size = dtype == COLI_F32 ? 4 : 2;
-  auto go = [&]<typename U>() {
-    const uint32_t units = (uint32_t)((int64_t)a.H * size / (int)sizeof(U));
-    const int64_t n = (int64_t)a.T * units;
-    auto kernel = n < ((int64_t)1 << 32) ? dispatch_kernel<U, false> : dispatch_kernel<U, true>;
-    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const U *)x, (uint32_t)a.T, a.k, units, a.pos,
-                       a.rows, (U *)xs);
-    return hipGetLastError();
-  };
-  if (whole(a.H, size, x, xs)) return go.template operator()<v4i32>();
-  return size == 4 ? go.template operator()<uint32_t>() : go.template operator()<uint16_t>();
+  if (dtype == COLI_F32) return launch_dispatch_t(a, (const uint32_t *)x, (uint32_t *)xs, s);
+  return launch_dispatch_t(a, (const uint16_t *)x, (uint16_t *)xs, s);
 }
 
 template <typename T>
 static hipError_t launch_combine_t(const PairArgs &a, const void *ys, const void *add, void *out, hipStream_t s) {
-  auto go = [&]<int VEC>() {
-    typedef piece_of<T, VEC> piece;
-    const uint32_t units = (uint32_t)(a.H / VEC);
+  return by_row<T>(a.H, [&]<int VEC, bool SHIFT>() {
+    const uint32_t H = a.H, units = (H + VEC - 1) / VEC;
     const int64_t n = (int64_t)a.T * units;
-    auto kernel = n < ((int64_t)1 << 32) ? pair_combine_kernel<T, VEC, false> : pair_combine_kernel<T, VEC, true>;
-    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const piece *)ys, a.rows, (uint32_t)a.T, a.k,
-                       units, a.pos, a.w, (const piece *)add, (piece *)out);
+    auto kernel = n < ((int64_t)1 << 32) ? pair_combine_kernel<T, VEC, SHIFT, false> : pair_combine_kernel<T, VEC, SHIFT, true>;
+    hipLaunchKernelGGL(kernel, dim3(groups_of((n + 255) / 256)), dim3(256), 0, s, (const T *)ys, a.rows, (uint32_t)a.T, a.k, H,
+                       units, a.pos, a.w, (const T *)add, (T *)out);
     return hipGetLastError();
-  };
-  return whole(a.H, sizeof(T), ys, out, add) ? go.template operator()<16 / sizeof(T)>() : go.template operator()<1>();
+  });
 }
 
 hipError_t launch_pair_combine(const PairArgs &a, int dtype, const void *ys, const void *add, void *out, hipStream_t s) {
@@ -368,14 +398,12 @@ hipError_t launch_pair_combine(const PairArgs &a, int dtype, const void *ys, con
 
 template <typename T>
 static hipError_t launch_grad_t(const PairArgs &a, const void *dout, const void *ys, void *dys, float *dw, hipStream_t s) {
-  auto go = [&]<int VEC>() {
-    typedef piece_of<T, VEC> piece;
-    const uint32_t units = (uint32_t)(a.H / VEC), P = (uint32_t)a.T * (uint32_t)a.k;
-    hipLaunchKernelGGL((combine_grad_kernel<T, VEC>), dim3(groups_of((P + 3) / 4)), dim3(256), 0, s, (const piece *)dout,
-                       (const piece *)ys, a.rows, P, a.k, units, a.pos, a.w, (piece *)dys, dw);
+  return by_row<T>(a.H, [&]<int VEC, bool SHIFT>() {
+    const uint32_t H = a.H, units = (H + VEC - 1) / VEC, P = (uint32_t)a.T * (uint32_t)a.k;
+    hipLaunchKernelGGL((combine_grad_kernel<T, VEC, SHIFT>), dim3(groups_of((P + 3) / 4)), dim3(256), 0, s, (const T *)dout,
+                       (const T *)ys, a.rows, P, a.k, H, units, a.pos, a.w, (T *)dys, dw);
     return hipGetLastError();
-  };
-  return whole(a.H, sizeof(T), dout, ys, dys) ? go.template operator()<16 / sizeof(T)>() : go.template operator()<1>();
+  });
 }
 
 hipError_t launch_pair_grad(const PairArgs &a, int dtype, const void *dout, const void *ys, void *dys, float *dw,

@@ -314,3 +314,46 @@ def test_more_elements_than_one_launch(q):
     dout, dy, dw = torch.randn((P, 1), device="cuda"), torch.empty((P, 1), device="cuda"), torch.empty((P, 1), device="cuda")
     q.combine_backward(dout, y, pos, w, dy, dw)
     assert torch.equal(dw, dout * y.flip(0)) and torch.equal(dy.flip(0), dout * w)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 7, 8, 9, 15, 17, 31, 510, 511, 513, 2047, 4646])
+def test_rows_of_no_whole_pieces(q, dtype, H):
+    """Row ends beside rows of NaN and guards: each element once, nothing outside. combine adds to out itself."""
+    import torch
+    T, k = 37, 3
+    rng = np.random.default_rng(H)
+    pos = (rng.permutation(T * k) * 2 + 1).astype(np.int32)  # every other row
+    pos[rng.random(T * k) < 0.2] = -1
+    ok = pos >= 0
+    R = 2 * T * k + 1
+    x = _t(rng.standard_normal((T, H)).astype(np.float32), dtype)
+    fenced = lambda n: torch.full((n * H + 16,), 3.0, dtype=_dt(dtype), device="cuda")  # noqa: E731
+    inside = lambda b, n: b[8:8 + n * H].view(n, H)  # noqa: E731
+    kept = lambda b, n: (b[:8] == 3).all() and (b[8 + n * H:] == 3).all()  # noqa: E731
+    rb = fenced(R)
+    rows = inside(rb, R)
+    q.dispatch(x, _t(pos), rows)
+    want = torch.full_like(rows, 3.0)
+    want[_t(pos[ok]).long()] = x[_t(np.arange(T * k)[ok] // k)]
+    assert torch.equal(rows, want) and kept(rb, R)
+    ys = torch.full_like(rows, float("nan"))
+    ys[_t(pos[ok]).long()] = _t(rng.standard_normal((int(ok.sum()), H)).astype(np.float32), dtype)
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    ob = fenced(T)
+    out = inside(ob, T)
+    out.copy_(x)
+    q.combine(ys, _t(pos), out, topk_w=_t(w), add=out)
+    want, size = _combine64(_n(ys), pos, w, _n(x), T, k)
+    tol = (k + 2) * U * size
+    assert (np.abs(_n(out) - want) <= tol + _half(dtype) * (np.abs(want) + tol) + _tiny(dtype)).all() and kept(ob, T)
+    db = fenced(R)
+    dys, dw = inside(db, R), torch.full((T, k), 7.0, device="cuda")
+    q.combine_backward(x, ys, _t(pos), _t(w), dys, dw)
+    g = _n(x)[np.arange(T * k) // k]
+    want = np.full((R, H), 3.0)
+    want[pos[ok]] = (g * w.reshape(-1, 1))[ok]
+    assert (np.abs(_n(dys) - want) <= (U + _half(dtype) * (1 + U)) * np.abs(want) + _tiny(dtype)).all() and kept(db, R)
+    terms = g[ok] * _n(ys)[pos[ok]]
+    got = _n(dw).reshape(-1)
+    assert (np.abs(got[ok] - terms.sum(1)) <= H * U * np.abs(terms).sum(1)).all() and (got[~ok] == 0).all()

@@ -83,10 +83,12 @@ __device__ __forceinline__ float i8_biased(int acc, float row, float channel, fl
 // silu(g) = g / (1 + e^-g) from t = e^-|g|, which does not overflow: g / (1 + t), or g t / (1 + t) below
 // 0, so that gates down to -103, where g t leaves fp32, count. t = 2^h (1 + l ln 2) with h + l =
 // -|g| log2(e) to about 2^-46, by the hardware's exponential and reciprocal (within 1 ulp each); t of
-// h below -64 is held times 2^64 (h + 64 is exact). One function for all kernels: the same bits in each.
+// h below -64 is held times 2^64 (h + 64 is exact, h being a value of its own: fused into x log2(e) + 64 it would
+// lose the rounding that l makes good, up to 46 half steps of t for 2). One function for all kernels: the same
+// bits in each.
 __device__ __forceinline__ float i8_silu(float g) {
   const float x = fmaxf(-fabsf(g), -200.0f);
-  const float h = x * 0x1.715476p+0f;
+  const float h = i8_product(x, 0x1.715476p+0f);
   const float l = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -h));
   const bool low = h < -64.0f;
   const float unit = low ? 0x1p-64f : 1.0f;

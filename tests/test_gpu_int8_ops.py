@@ -418,3 +418,42 @@ def test_experts_one_token_as_in_a_batch(q):
         # the few-row kernel's silu and the tiled one's may differ by a few steps
         near = lambda x, y: ((x - y).abs() <= 2.0 ** -20 * y.abs() + 2.0 ** -126).all()  # noqa: E731
         assert near(h1[:n * k], h[a * k:b * k]) and near(h1[n * k:], h[T * k + a:T * k + b])
+
+
+# T, k, E: one token (gate and up rows in half tiles), few rows, tiles over the route
+@pytest.mark.parametrize("T,k,E", [(1, 2, 8), (5, 2, 8), (130, 2, 4)])
+def test_gate_up_silu_of_any_gate(q, T, k, E):
+    """Gates from -103.5, where silu is among fp32's smallest numbers, to 20: known exactly, since a row has
+    one value, so that only silu's own roundings and the product's are left."""
+    import torch
+    rng = np.random.default_rng(T)
+    H, F, up = 128, 1280, 96.0
+    want_gate = np.linspace(-103.5, 20.0, F)
+    want_gate[-100:] = np.linspace(-44.6, -44.2, 100)
+    codes = np.zeros((E + 1, 3 * F * H), np.int8)
+    scales = np.ones((E + 1, 2 * F + H), np.float32)
+    for e in range(E + 1):
+        mine = rng.permutation(want_gate)
+        codes[e, :F * H:H] = np.where(mine < 0, -127, 127)
+        codes[e, F * H:2 * F * H:H] = 127
+        scales[e, :F] = np.abs(mine) / 127
+        scales[e, F:2 * F] = up / 127
+    x = torch.zeros((T, H), device="cuda")
+    x[:, 0] = 1.0  # scale 1 / 127, code 127
+    row = np.float32(1.0) / np.float32(127.0)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    cfg = q.make_cfg(H, F, E, k, has_shared=True, wbits=8)
+    h = torch.full((T * (k + 1), F), 9.0, device="cuda")
+    q.int8_gate_up(cfg, q.Weights(_t(codes), _t(scales), None, None), x, **_grouped(q, idx, E), h=h,
+                   workspace=q.alloc_int8_experts_workspace(cfg, T))
+    got = _n(h)
+    for e, rows, _ in _rows_of(idx, E, True):
+        sign = codes[e, :F * H:H].astype(np.float32)
+        gate = (sign * 127 * (row * scales[e, :F])).astype(np.float64)  # an fp32 product each, as the kernels have it
+        u = np.float64(np.float32(127 * 127) * (row * scales[e, F:2 * F]))
+        silu = gate / (1 + np.exp(-gate))
+        # relative, half steps U: the hardware's exponential 2 and the sum with its correction 1 (e^-|g|), 1 + e^-|g| 1,
+        # its reciprocal 2, two products 2, the product with up 1; the correction's own terms (ln 2 l of 2^-16,
+        # rounded, and its square) below 2^-34. Subnormal results: half a step of 2^-149 of silu and of h.
+        tol = 9.1 * U * np.abs(silu * u) + 2.0 ** -150 * (np.abs(u) + 1)
+        assert (np.abs(got[rows] - silu * u) <= tol).all(), e

@@ -457,3 +457,65 @@ def test_gate_up_silu_of_any_gate(q, T, k, E):
         # rounded, and its square) below 2^-34. Subnormal results: half a step of 2^-149 of silu and of h.
         tol = 9.1 * U * np.abs(silu * u) + 2.0 ** -150 * (np.abs(u) + 1)
         assert (np.abs(got[rows] - silu * u) <= tol).all(), e
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_gate_up_same_bits_in_every_kernel(q, dtype):
+    """A row of h is the same to the bit in the half-tile kernel of one token, the few-row and the tiled one."""
+    import torch
+    rng = np.random.default_rng(11)
+    T, H, F, E, k = 300, 512, 384, 8, 3
+    idx, _, codes, scales = _case(rng, T, H, F, E, k, True, False)
+    scales[:, :F] *= 6  # gates past -44 and -88 too
+    cfg = q.make_cfg(H, F, E, k, has_shared=True, wbits=8)
+    wt = q.Weights(_t(codes), _t(scales), None, None)
+    x = _rows(rng, T, H, dtype)
+    ws = q.alloc_int8_experts_workspace(cfg, T)
+
+    def run(a, b):
+        h = torch.zeros(((b - a) * (k + 1), F), dtype=_dt(dtype), device="cuda")
+        q.int8_gate_up(cfg, wt, x[a:b].contiguous(), **_grouped(q, idx[a:b], E), h=h, workspace=ws)
+        return h
+
+    h = run(0, T)
+    for a, b in ((0, 1), (299, 300), (7, 9), (100, 130), (100, 140)):  # one token, few rows (up to 12 pairs an expert), tiles
+        n, part = b - a, run(a, b)
+        assert torch.equal(part[:n * k], h[a * k:b * k]) and torch.equal(part[n * k:], h[T * k + a:T * k + b]), (a, b)
+
+
+@pytest.mark.parametrize("H,F", [(128, 7040), (7040, 128)])
+def test_experts_offsets_past_31_bits(q, H, F):
+    """The most pairs with the widest rows: 131070 rows of 7040 fp32 values are 3.7 GB of h or of the down product's
+    rows, near the most that 32-bit offsets reach. Every row as in slices of the batch."""
+    import torch
+    T, E, k = 65535, 3, 1
+    rng = np.random.default_rng(H)
+    idx, w, codes, scales = _case(rng, T, H, F, E, k, True, False)
+    idx[::7] = -1
+    cfg = q.make_cfg(H, F, E, k, has_shared=True, wbits=8)
+    wt = q.Weights(_t(codes), _t(scales), None, None)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    x = torch.randn((T, H), device="cuda", generator=g)
+    hd = torch.randn((2 * T, F), device="cuda", generator=g) if F < H else None
+    ids, tw = _t(idx), _t(w)
+
+    def run(a, b):
+        n, group = b - a, _grouped(q, idx[a:b], E)
+        ws = q.alloc_int8_experts_workspace(cfg, n)
+        if hd is None:
+            h = torch.full((2 * n, F), 9.0, device="cuda")
+            q.int8_gate_up(cfg, wt, x[a:b], **group, h=h, workspace=ws)
+            return h[:n], h[n:]
+        out = torch.full((n, H), 9.0, device="cuda")
+        q.int8_down(cfg, wt, torch.cat([hd[a:b], hd[T + a:T + b]]), ids[a:b], tw[a:b], **group, out=out, workspace=ws)
+        return (out,)
+
+    whole = run(0, T)
+    for a in range(0, T, 8192):
+        b = min(T, a + 8192)
+        for i, (part, all_) in enumerate(zip(run(a, b), whole)):
+            assert torch.equal(part, all_[a:b]), (i, a)
+    assert not any(v.isnan().any() for v in whole)
+    if hd is None:
+        assert (whole[0][::7] == 9.0).all() and (whole[0][1::7] != 9.0).any(1).all()

@@ -172,7 +172,9 @@ int coli_moe_group(const coli_moe_cfg *cfg, const int32_t *topk_idx, int32_t T, 
 /* Expert FFNs over the batch union and the combine, given a route and its
  * grouping (the outputs of coli_moe_route and coli_moe_group for the same T):
  * quantises x (Q8_0), runs gate/up with fused SiLU*up and Q8_0 requantisation,
- * runs down, then out fp32 [T][H] = slot-order weighted sum + shared expert.
+ * runs down, then out fp32 [T][H] = slot-order weighted sum + shared expert. Empty slots (-1)
+ * have weight 0, as coli_moe_route leaves them; a route with other ids (n_active = -1) is not
+ * for this call, whose out is then unspecified.
  * Follows the router, batch-union, quantization-kernel and integer-dot items of
  * colibri-strix README, "What's implemented". */
 int coli_moe_ffn(const coli_moe_cfg *cfg, const coli_moe_weights *w, const float *x, int32_t T,
@@ -281,6 +283,8 @@ int coli_moe_mxfp4_linear(const void *x, int dtype, const uint8_t *codes, const 
  *     token t, row T k + t the shared expert's. Rows of empty slots (-1) are not written.
  *   down: out [T][H] = sum_j w_tj y_tj in slot order + y_shared, y = down rows . MXFP4(h row);
  *     h rows of empty slots do not enter.
+ * A slot whose id is neither an expert nor -1 is an empty one too (n_active is -1 then; expert_off,
+ * pair_perm and active, as coli_moe_group and coli_moe_sort_pairs leave them, hold the other pairs).
  * x, h, out of one dtype and 16-byte aligned. workspace:
  * coli_moe_mxfp4_experts_workspace_bytes(cfg, T_max) (0 if invalid), 256-byte aligned, for
  * either half and every T <= T_max.

@@ -101,8 +101,7 @@ __global__ __launch_bounds__(256, ACT == I8_ACT_X || NT == 4 ? 2 : 4) void i8_ge
     if (u < 0) {
       e = a.E;
     } else {
-      const int na = max(0, min(*a.nact, a.E));
-      if (u >= na) return;
+      if (const int na = *a.nact; u >= na && (na >= 0 || u >= hit_experts(a.nact, a.off, a.E))) return;
       e = a.active[u];
       first = a.off[e];
       n = a.off[e + 1] - first;

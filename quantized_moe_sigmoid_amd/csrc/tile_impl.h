@@ -108,7 +108,7 @@ template <typename Args>
 __global__ __launch_bounds__(1024) void route_tiles_kernel(Args a, int bm, int cap) {
   __shared__ int wsum[16];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int na = max(0, min(*a.nact, a.E));
+  const int na = hit_experts(a.nact, a.off, a.E);
   const int shared = a.has_shared ? (a.M + bm - 1) / bm : 0;
   int e = 0, first = 0, n = 0;
   if (tid < na) {

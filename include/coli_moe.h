@@ -98,7 +98,7 @@ typedef enum {
 
 typedef enum { COLI_W_INT2 = 2, COLI_W_INT4 = 4, COLI_W_INT8 = 8, COLI_W_MXFP4 = 40 } coli_wfmt;
 
-/* Layer shape. Limits: hidden and ffn multiples of 128; 1 <= n_experts <= 1024;
+/* Layer shape. Limits: hidden and ffn multiples of 128 up to 7040; 1 <= n_experts <= 1024;
  * n_experts % n_group == 0; 1 <= topk_group <= n_group <= 64;
  * 1 <= top_k <= min(64, topk_group * n_experts / n_group); has_shared 0 or 1;
  * wfmt 2, 4, 8 (scale_group 0 or 64) or COLI_W_MXFP4 (scale_group 32); 0 <= topp <= 1. */
@@ -355,7 +355,8 @@ int coli_moe_int8_down(const coli_moe_cfg *cfg, const coli_moe_weights *w, const
  *     empty slot). dys or dtopk_w may be NULL: not wanted. ys may be NULL without dtopk_w.
  * A place outside [0, rows) is an empty slot; rows that no pair has are not written (so rows may be
  * more than the pairs). A place may stand once. xs, ys, x, out, add, dout and dys of one dtype, any H,
- * aligned to their type (rows of whole aligned 16 bytes run fastest); T k < 2^30, T H < 2^40. */
+ * aligned to their type (rows of whole aligned 16 bytes run fastest); T k < 2^30, T H and rows H < 2^40.
+ * Outputs lie apart from the inputs, but for add. */
 size_t coli_moe_sort_pairs_workspace_bytes(int64_t P, int32_t n_experts);
 int coli_moe_sort_pairs(const int32_t *topk_idx, int32_t T, int32_t k, int32_t n_experts, int32_t *expert_off,
                         int32_t *pair_perm, int32_t *pair_pos, int32_t *active, int32_t *n_active, void *workspace,

@@ -15,6 +15,13 @@ constexpr int GEMV_ROWS = 32;       // rows per workgroup tile of the GEMV kerne
 constexpr int GEMV_NT = 8;          // tokens handled per pass of the GEMV kernels
 constexpr int ROUTE_KC = 256;       // K chunk of the router logits kernel (decode tiling)
 
+// LDS of a decode-sized workgroup for rows of K inputs, whose limit is that of hidden and ffn (7040)
+constexpr size_t GEMV_LDS_LIMIT = 64 * 1024;
+constexpr size_t gemv_lds(int K) {
+  return (size_t)GEMV_NT * K + (size_t)GEMV_NT * (K / QK) * sizeof(float) + (size_t)GEMV_NT * GEMV_ROWS * sizeof(float) +
+         2 * GEMV_NT * sizeof(int);
+}
+
 constexpr int W_MX = COLI_W_MXFP4;  // MXFP4 weights: 4-bit E2M1 codes, one E8M0 byte per 32 inputs
 
 // Packed bytes of one row of n inputs.

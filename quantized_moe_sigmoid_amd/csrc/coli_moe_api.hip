@@ -39,13 +39,6 @@ WsLayout ws_layout(const coli_moe_cfg &c, int32_t T, int32_t ksplit) {
   return L;
 }
 
-static constexpr size_t GEMV_LDS_LIMIT = 64 * 1024;
-
-static size_t gemv_lds(int K) {
-  return (size_t)GEMV_NT * K + (size_t)GEMV_NT * (K / QK) * sizeof(float) + (size_t)GEMV_NT * GEMV_ROWS * sizeof(float) +
-         2 * GEMV_NT * sizeof(int);
-}
-
 int check_cfg(const coli_moe_cfg *c) {
   if (!c) return COLI_E_INVALID;
   if (c->hidden <= 0 || c->ffn <= 0 || c->n_experts <= 0 || c->top_k <= 0 || c->n_group <= 0 ||

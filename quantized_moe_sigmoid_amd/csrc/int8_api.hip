@@ -81,25 +81,31 @@ static I8Args expert_args(const coli_moe_cfg &c, const coli_moe_weights &w, int3
 static bool i8_linear_tiled(int32_t M, int32_t N) { return M > 48 || (M > 8 && (int64_t)M * N > 150000); }
 
 // The kernel for few rows reads an expert's weights once for each 16 rows, the tiled one fills the card
-// with about eight tiles to a CU and reads faster then. us, few rows and tiled, gate/up and down:
-//   256 experts of 6144 x 2048, 8 to a token, and a shared one:
-//     17 tokens                                              483 and 447    253 and 257
-//     24 tokens                                              547 and 516    316 and 304
-//     64 tokens                                              1015 and 903   543 and 512
-//   64 of 2048 x 1024, 8 to a token: 17, 64, 200 tokens      48, 57, 104 and 49, 56, 57   37, 43, 75 and 43, 48, 52
-//   32 of 1024 x 512: 300 tokens                             15 and 20      15 and 20
-//   8 of 4096 x 2048: 64, 128 tokens                         36, 48 and 38, 42   23, 30 and 29, 30
-//   8 of 6144 x 2048, 2 to a token: 200 tokens               140 and 66     92 and 41
+// with about eight tiles to a CU and reads faster then. us, few rows and tiled, of bf16 (events; down with its
+// quantisation and combine):
+//   experts, slots to a token                    tokens  gate/up        down
+//   256 of 6144 x 2048, 8 and a shared one       17      436 and 406    248 and 243
+//                                                24      606 and 566    313 and 302
+//                                                64      1013 and 901   494 and 467
+//   64 of 2048 x 1024, 8 and a shared one        17      54 and 58      37 and 43
+//                                                64      65 and 73      44 and 51
+//                                                200     112 and 75     80 and 56
+//   32 of 1024 x 512, 1                          300     15 and 20      17 and 20
+//   8 of 4096 x 2048, 1                          64      38 and 46      24 and 29
+//                                                128     49 and 48      31 and 30
+//   8 of 6144 x 2048, 2                          200     138 and 66     93 and 40
 // (64 x 64 and 64 x 128 tiles over a route: slower than either but for 600 tokens over 32 of 1024 x 512, 24 and 26.)
 static bool i8_experts_tiled(const I8Args &a) {
   const int64_t P = (int64_t)a.M * a.k, hit = std::min<int64_t>(P, a.E);
   return P > 12 * (int64_t)a.E || (P > 128 && hit * a.N >= 2048 * 128);
 }
 
+// The tiled kernel's offsets into the activations and the output have 32 bits, which check_cfg's and check_T's
+// limits keep: at most 65535 pairs and as many tokens, rows of fewer than 7168 values of 4 bytes.
+static_assert(gemv_lds(7168) > GEMV_LDS_LIMIT && 2 * 65535ll * 7168 * 4 < (1ll << 32) - 65536);
+
 static hipError_t launch_experts(I8Mode mode, int dtype, I8Args &a, uint8_t *ws, const I8Ws &L, hipStream_t s) {
-  // the tiled kernel's offsets into the activations and the output have 32 bits
-  const int64_t rows = (int64_t)a.M * (a.k + a.has_shared), widest = std::max<int64_t>((int64_t)a.N * 4, i8_padded(a.K));
-  if (!i8_experts_tiled(a) || rows * widest >= ((int64_t)1 << 32) - 65536) return launch_i8_gemv(mode, dtype, a, s);
+  if (!i8_experts_tiled(a)) return launch_i8_gemv(mode, dtype, a, s);
   a.tiles = reinterpret_cast<int4 *>(ws + L.tiles);
   a.ntiles = reinterpret_cast<int32_t *>(ws + L.ntiles);
   return launch_i8_tile(mode, dtype, a, s);

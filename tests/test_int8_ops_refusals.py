@@ -202,3 +202,11 @@ def test_definition_of_sorted_pairs():
     off, perm, pos, active = i8ref.sort_pairs(np.array([[2, 0], [-1, 2], [0, 5]]), 4)
     assert off.tolist() == [0, 2, 2, 4, 4] and perm.tolist() == [1, 4, 0, 3]
     assert pos.tolist() == [2, 0, -1, 3, 1, -1] and active.tolist() == [0, 2]
+
+
+@pytest.mark.parametrize("shape", [dict(hidden=7168, ffn=128), dict(hidden=128, ffn=7168)])
+def test_experts_widths_that_offsets_rest_on(q, shape):
+    """Rows wider than 7040 are refused: 131070 of 7040 fp32 values are what the kernels' 32-bit offsets reach."""
+    need = lambda c: q.lib().coli_moe_int8_experts_workspace_bytes(C.byref(c), 65535)  # noqa: E731
+    assert need(q.make_cfg(n_experts=3, top_k=1, has_shared=True, wbits=8, **shape)) == 0
+    assert need(q.make_cfg(n_experts=3, top_k=1, has_shared=True, wbits=8, **{n: v - 128 if v > 128 else v for n, v in shape.items()})) > 0

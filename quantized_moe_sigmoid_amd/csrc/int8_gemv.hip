@@ -7,12 +7,12 @@
 // straight into the operand registers; their integer sums meet in LDS. One row of activations (x in
 // ACT_X) is quantised by every workgroup itself while its first two groups of weights are under way,
 // which saves a launch. bf16: one row of 12288 x 6144 13 us (75 MB, 12 us at the 6.3 TB/s of a plain read);
-// gate/up of one token over 9 experts of 6144 x 2048 43 to 47 us (226 MB), of 16 tokens over 256 406 to 420
-// us (6.1 to 6.4 TB/s). One group under way and four workgroups to a CU where activations come from the
+// gate/up of one token over 9 experts of 6144 x 2048 43 to 49 us by the card (226 MB), of 16 tokens over 256 406 to
+// 423 (2.58 GB, 6.1 to 6.3 TB/s). One group under way and four workgroups to a CU where activations come from the
 // workspace: gate/up of 16 tokens over 64 experts of 2048 x 1024 60 -> 52 us, of 256 the same.
 //
-// i8_down_kernel: 16 tokens over 256 experts of 6144 x 2048 232 us (1.29 GB, 5.6 TB/s with the quantisation's
-// launch), one token 24 (113 MB; a bare read of them in this order takes 18.6).
+// i8_down_kernel: 16 tokens over 256 experts of 6144 x 2048 232 to 241 us (1.29 GB, 5.4 to 5.6 TB/s with the
+// quantisation's launch), one token 23 to 27 (113 MB; a bare read of them in this order takes 18.6).
 #include "int8_impl.h"
 
 namespace coli {

@@ -5,16 +5,19 @@
 // The sums stay in the instruction's int32 accumulators over all of K, so the inner loop has no work
 // for the vector units; scales, bias and SiLU*up come in at the end.
 //
-// Dense, 4093 x 12288 x 6144 bf16: 273 to 298 us with the quantisation's 19 (2.4 POP/s in the kernel). The
-// instruction on random codes in registers alone reaches 2.9 to 3.5 POP/s here (4.9 on zeros: the card's
-// power is the limit). Without loads 262 us, without products 245, of 290. A wavefront's 128 x 128 part
-// fills the accumulators; a row of a stage is one 128-byte line.
+// Dense, 4093 x 12288 x 6144 bf16: 273 to 298 us by the card, with the quantisation's 19 to 23 (2.1 to 2.3
+// POP/s). The instruction on random codes in registers alone reaches 2.9 to 3.5 POP/s here (4.9 on zeros: the
+// card's power is the limit), 177 to 213 us. Of 281 us in all 234 are left without loads and 211 without products: they
+// overlap but for 47, with one wavefront to a SIMD, whose 128 x 128 part fills the accumulators (and spills 14
+// registers outside the loop over the stages). A row of a stage is one 128-byte line.
 //
-// Over a route, 2048 tokens, 256 experts of 6144 x 2048 and a shared one, Zipf-like: gate/up 1268 to 1300
-// us, down 745 (and 78 for the combine, 20 for the quantisation of h). Bound by the weights' way from HBM:
-// without products or LDS reads the same. Column strips of 1, 2 and 4 tiles 1344, 1381 and 1459 us;
-// weights that one row tile alone reads past the caches 1344 -> 1300 (all weights: 1344, row tiles that share
-// them meet in the L2); results past the caches 1307 -> 1283.
+// Over a route, 2048 tokens, 256 experts of 6144 x 2048 and a shared one, Zipf-like: gate/up 1268 to 1380 us by the
+// card, down 739 to 773 (and 77 to 83 for the combine, 20 for the quantisation of h). Bound by the loads' way:
+// of 1277 us for gate/up 1259 are left without products and 699 without loads, of 845 for the whole down 848 and 549.
+// Gate/up fetches 6.9 GB (6.5 needed), down 3.3 (3.2); a kernel that only moves gate/up's bytes to LDS takes 910
+// to 1030, so that the rest is the tiles' starts and ends, one workgroup to a CU. Column strips of 1, 2 and 4 tiles
+// 1344, 1381 and 1459 us; weights that one row tile alone reads past the caches 1344 -> 1300 (all weights: 1344, row
+// tiles that share them meet in the L2); results past the caches 1307 -> 1283.
 #include "int8_impl.h"
 #include "mxfp4_tile_plan.h"
 #include "tile_impl.h"
@@ -276,7 +279,8 @@ __global__ __launch_bounds__(256, S::OCC) void i8_tile_kernel(I8Args a) {
       // 8 (r / 4) + 4 hh + r % 4, so that a lane holds runs of four output columns of a row. They go
       // through LDS, up to 128 bytes of 32 rows at a time, so that a store covers whole lines: written
       // from the accumulators, a run each, 32 rows' stores of 32 bytes go out at a time (down of 2048 tokens
-      // 872 us and 854 so, 752 without stores; 4093 x 12288 x 6144 299, 290 and 272).
+      // 872 us and 854 so, 752 without stores; 4093 x 12288 x 6144 299, 290 and 272, all before the loads and stores past
+      // the caches).
       // The stores have no branch (it would bring all results out of the accumulators at once,
       // as it does for a ragged N, whose last piece's columns go one by one): lanes without a row,
       // and pieces past the last column, give an offset past the buffer's end, where a store is

@@ -222,9 +222,9 @@ __device__ __forceinline__ void split(int64_t i, uint32_t units, int64_t &row, u
 
 constexpr int SLOTS = 8;  // rows of a token under way at a time (combine of 2048 x 8 rows of 6144: 4: 42.5 us, 8: 41)
 
-// 8191 tokens, 8 slots, 2048 bf16: 50 us, 268 MB written at 5.4 TB/s. By pair, x read eight times through
-// the L2s of other XCDs: 73. Rows of no whole pieces meet in lines, which the L2 puts together: 6915 tokens, 8
-// slots, 406 fp32, with the sort 29 us, past the caches 36, by element 41.
+// 8191 tokens, 8 slots, 2048 bf16: 50 to 55 us by the card, 268 MB written and 35 read at 5.5 TB/s. By pair, x
+// read eight times through the L2s of other XCDs: 73. Rows of no whole pieces meet in lines, which the L2 puts
+// together: 6915 tokens, 8 slots, 406 fp32, with the sort 29 us, past the caches 36, by element 41 (one card).
 template <typename T, int VEC, bool SHIFT, bool WIDE>
 __global__ __launch_bounds__(256) void dispatch_kernel(const T *__restrict__ x, uint32_t T_, int k, uint32_t H, uint32_t units,
                                                        const int32_t *__restrict__ pos, int64_t rows,
@@ -250,8 +250,10 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const T *__restrict__ x, 
   }
 }
 
-// 2048 tokens, 8 slots of which a fifth is empty, 6144 fp16, a row added: 40 us, 211 MB at 5.3 TB/s; row loads
-// that fill the caches 49, empty slots' loads sent to row 0 instead of left out 41. add may be out.
+// 2048 tokens, 8 slots of which a fifth is empty, 6144 fp16, a row added: 40 to 45 us by the card, 211 MB at 4.7
+// to 5.3 TB/s; row loads that fill the caches 49, empty slots' loads sent to row 0 instead of left out 41. 4095
+// tokens, 8 slots, 2047 bf16: 36 to 40, 140 MB read where 134 are needed: the lines that rows share are not what it
+// waits for. add may be out.
 template <typename T, int VEC, bool SHIFT, bool WIDE>
 __global__ __launch_bounds__(256) void pair_combine_kernel(const T *__restrict__ ys, int64_t rows, uint32_t T_, int k, uint32_t H,
                                                            uint32_t units, const int32_t *__restrict__ pos,
@@ -299,8 +301,9 @@ __global__ __launch_bounds__(256) void pair_combine_kernel(const T *__restrict__
   }
 }
 
-// A wavefront takes a pair: its row of the gradient, and the weight's. 4093 tokens, 8 slots, 2048 fp32: 102
-// us, 570 MB at 5.6 TB/s.
+// A wavefront takes a pair: its row of the gradient, and the weight's. 4093 tokens, 8 slots, 2048 fp32: 101
+// to 110 us by the card, 606 MB moved (570 needed) at 5.6 TB/s. A turn loads 512 pieces and shorter rows repeat their
+// last one, so that 16-bit rows of 2048 have half as much under way: 54 us, 285 MB needed; of 2047 80 us.
 constexpr int GRAD_AHEAD = 8;  // pieces of a lane under way: 2, 4, 8, 16: 126, 114, 104, 443 us
 template <typename T, int VEC, bool SHIFT>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const T *__restrict__ dout, const T *__restrict__ ys, int64_t rows,
